@@ -229,7 +229,7 @@ def _times(x, *fs):
 
 def _plain_fwd(s, alpha, beta, f):
     """The float32 states h [*, T, D] and the final states."""
-    u = _times(s["x"].float(), f, beta)
+    u = _times(s["x"].float(), f, beta).clone()  # the inputs stay as they are
     if s["cu"]:
         seq = s["seq"]
         u[seq["first"]] += alpha[seq["first"]] * s["h0"][seq["full"]]
@@ -247,7 +247,7 @@ def _plain_fwd(s, alpha, beta, f):
 def _plain_bwd(s, gates, h, cut):
     g, slope, alpha, beta, f = gates
     case, cu = s["case"], s["cu"]
-    dh = s["dh"].float()
+    dh = s["dh"].float().clone()
     if cu:
         seq = s["seq"]
         dh[seq["last"]] += s["dht"][seq["full"]]
