@@ -9,10 +9,13 @@ every call raises if the library reports an error.
 Entry points (same names as the C ABI):
     gdn_gate_prep, gdn_chunk_fwd, gdn_chunk_workspace_bytes, gdn_chunk_fwd_noalloc,
     gdn_recurrent_step, gdn2_chunk_fwd, gdn_check_status
+and, with the vector state, gdn_linrec_fwd, gdn_linrec_bwd, gdn_linrec_step; for q and k,
+gdn_qk_norm_rope, gdn_qk_norm_rope_bwd.
 """
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -24,9 +27,13 @@ __all__ = ["gdn_gate_prep", "gdn_chunk_fwd", "gdn_chunk_workspace_bytes", "gdn_r
            "gdn2_chunk_fwd", "gdn2_chunk_workspace_bytes", "gdn_chunk_fwd_noalloc",
            "gdn_chunk_fwd_gated_norm", "gdn_recurrent_step_gated_norm",
            "gdn_chunk_bwd", "gdn_chunk_bwd_workspace_bytes",
+           "gdn_linrec_fwd", "gdn_linrec_bwd", "gdn_linrec_step", "gdn_linrec_chunks",
+           "gdn_linrec_workspace_bytes", "gdn_linrec_bwd_workspace_bytes",
+           "gdn_qk_norm_rope", "gdn_qk_norm_rope_bwd", "gdn_qk_norm_rope_bwd_workspace_bytes",
            "gdn_check_status", "gdn_status", "gdn_test_set_wait_fault", "GDNError",
            "LIB_PATH", "lib", "F32", "BF16",
-           "QK_L2NORM", "GATES_PRECOMPUTED", "OUT_F32"]
+           "QK_L2NORM", "GATES_PRECOMPUTED", "OUT_F32", "LINREC_TIED", "LINREC_UNIT",
+           "GRAD_F32", "QK_RMSNORM", "ROPE_INTERLEAVED", "LINREC_CHUNK"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libgdn.so")
@@ -40,11 +47,14 @@ lib = ctypes.CDLL(LIB_PATH)
 
 F32, BF16 = 0, 1
 QK_L2NORM, GATES_PRECOMPUTED, OUT_F32 = 1, 2, 4
+LINREC_TIED, LINREC_UNIT, GRAD_F32, QK_RMSNORM, ROPE_INTERLEAVED = 8, 16, 32, 64, 128
+LINREC_CHUNK = 64
 _STATUS = {0: "GDN_OK", -1: "GDN_ERR_INVALID_ARG", -2: "GDN_ERR_UNSUPPORTED",
            -3: "GDN_ERR_CUDA", -4: "GDN_ERR_TIMEOUT", -5: "GDN_ERR_WORKSPACE",
            -6: "GDN_ERR_RANGE"}
 
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_ll = ctypes.c_longlong
 lib.gdn_gate_prep.argtypes = [_vp, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f,
                               _vp, _vp, _vp, _vp, _vp]
 lib.gdn_chunk_fwd.argtypes = [_vp] * 8 + [_i] * 7 + [_f, _i, _vp, _vp, _vp, _sz, _vp]
@@ -73,6 +83,22 @@ lib.gdn_recurrent_step_gated_norm.argtypes = [_vp] * 10 + [_f, _vp] + [_i] * 6 +
 lib.gdn_chunk_bwd.argtypes = [_vp] * 10 + [_i] * 7 + [_f, _i] + [_vp] * 9 + [_sz, _vp]
 lib.gdn_chunk_bwd_workspace_bytes.argtypes = [_i] * 6
 lib.gdn_chunk_bwd_workspace_bytes.restype = _sz
+lib.gdn_linrec_fwd.argtypes = ([_vp] * 7 + [_i] * 3 + [_ll] * 3 + [_i, _i, _vp, _ll] + [_vp] * 3
+                               + [_sz, _vp])
+lib.gdn_linrec_bwd.argtypes = ([_vp] * 7 + [_i] * 3 + [_ll] * 3 + [_vp, _ll, _vp, _vp, _i, _i]
+                               + [_vp, _ll] * 3 + [_vp] * 4 + [_sz, _vp])
+lib.gdn_linrec_step.argtypes = [_vp] * 6 + [_i] * 2 + [_ll] * 3 + [_i, _i, _vp, _ll, _vp]
+lib.gdn_linrec_workspace_bytes.argtypes = [_vp, _i, _i, _i]
+lib.gdn_linrec_workspace_bytes.restype = _sz
+lib.gdn_linrec_bwd_workspace_bytes.argtypes = [_vp, _i, _i, _i, _i, _i]
+lib.gdn_linrec_bwd_workspace_bytes.restype = _sz
+lib.gdn_qk_norm_rope.argtypes = ([_vp] * 6 + [_ll] + [_i] * 4 + [_ll] * 2 + [_i, _i, _f, _f]
+                                 + [_vp, _ll] * 2 + [_vp])
+lib.gdn_qk_norm_rope_bwd.argtypes = ([_vp] * 6 + [_ll] + [_i] * 4 + [_ll] * 2 + [_vp, _ll] * 2
+                                     + [_i, _i, _f, _f] + [_vp, _ll] * 2 + [_vp] * 3
+                                     + [_sz, _vp])
+lib.gdn_qk_norm_rope_bwd_workspace_bytes.argtypes = [_ll] + [_i] * 4
+lib.gdn_qk_norm_rope_bwd_workspace_bytes.restype = _sz
 lib.gdn_check_status.argtypes = [_vp]
 lib.gdn_test_set_wait_fault.argtypes = [_i, ctypes.c_uint]
 lib.gdn_test_set_wait_fault.restype = _i
@@ -84,6 +110,8 @@ for _fn in (lib.gdn_gate_prep, lib.gdn_chunk_fwd, lib.gdn_chunk_fwd_noalloc, lib
             lib.gdn2_chunk_fwd,
             lib.gdn_recurrent_step, lib.gdn_conv_prefill, lib.gdn_rmsnorm_gated,
             lib.gdn_kda_chunk_fwd, lib.gdn_chunk_fwd_varlen,
+            lib.gdn_linrec_fwd, lib.gdn_linrec_bwd, lib.gdn_linrec_step,
+            lib.gdn_qk_norm_rope, lib.gdn_qk_norm_rope_bwd,
             lib.gdn_check_status, lib.gdn_version):
     _fn.restype = _i
 
@@ -612,6 +640,343 @@ def gdn_rmsnorm_gated(o, z, weight, *, eps=1e-6, y=None, stream=None):
     return y
 
 
+# ---- the gated linear recurrence and the norm-and-rotation of q and k ----------------------
+
+
+def _on_device(fn):
+    """Runs an entry point on its first argument's device and on `stream` (default: that
+    device's current stream); what it allocates then belongs to that stream."""
+    @functools.wraps(fn)
+    def call(first, *args, stream=None, **kw):
+        if not first.is_cuda:
+            raise ValueError("tensor must live on a CUDA device")
+        dev = first.device
+        if stream is None and dev.index == torch.cuda.current_device():
+            return fn(first, *args, **kw)
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"stream of {stream.device} for tensors of {dev}")
+        with torch.cuda.device(dev), torch.cuda.stream(stream):
+            return fn(first, *args, **kw)
+    return call
+
+
+def _dense(t, dtype, shape, dev, name):
+    """Pointer of a contiguous tensor of this dtype, shape and device (None -> NULL)."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name}: on {t.device}, expected {dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
+def _strided(t, dtype, shape, dev, name, tail=1):
+    """(pointer, elements from one token to the next) of a tensor of one or two token axes
+    and `tail` dense axes: a view whose tokens are a fixed distance apart, at least a
+    token's elements (None -> (NULL, 0))."""
+    if t is None:
+        return None, 0
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name}: on {t.device}, expected {dev}")
+    st, n = t.stride(), t.dim()
+    row = 1
+    for i in range(n - 1, n - 1 - tail, -1):
+        if shape[i] > 1 and st[i] != row:
+            raise ValueError(f"{name}: the elements of a token must be contiguous")
+        row *= shape[i]
+    ld = row
+    if t.numel() > 0:
+        lead = n - tail
+        if shape[lead - 1] > 1:
+            ld = st[lead - 1]
+            if lead == 2 and shape[0] > 1 and st[0] != ld * shape[1]:
+                raise ValueError(f"{name}: the tokens must be a fixed distance apart")
+        elif lead == 2 and shape[0] > 1:
+            ld = st[0]
+        if ld < row:
+            raise ValueError(f"{name}: tokens overlap (a broadcast view?)")
+    return t.data_ptr(), ld
+
+
+_SCALES = {"none": 0, "tied": LINREC_TIED, "unit": LINREC_UNIT}
+
+
+def _host_offsets(cu_seqlens):
+    """(ctypes int64 array or None, sequences)."""
+    if cu_seqlens is None:
+        return None, 0
+    if hasattr(cu_seqlens, "tolist"):
+        cu_seqlens = cu_seqlens.tolist()
+    n = len(cu_seqlens)
+    if n < 1:
+        raise ValueError("cu_seqlens must hold the sequences' offsets and their end")
+    return (_ll * n)(*cu_seqlens), n - 1
+
+
+def gdn_linrec_chunks(B, T, cu_seqlens=None) -> int:
+    """Rows of `states`: the chunks of LINREC_CHUNK tokens of all sequences."""
+    if cu_seqlens is None:
+        return B * (-(-T // LINREC_CHUNK))
+    cu = cu_seqlens.tolist() if hasattr(cu_seqlens, "tolist") else cu_seqlens
+    return sum(-(-(int(b) - int(a)) // LINREC_CHUNK) for a, b in zip(cu, cu[1:]))
+
+
+def gdn_linrec_workspace_bytes(B, T, D, cu_seqlens=None) -> int:
+    """Bytes of device workspace gdn_linrec_fwd needs (T: all packed tokens)."""
+    return int(lib.gdn_linrec_workspace_bytes(_host_offsets(cu_seqlens)[0], B, T, D))
+
+
+def gdn_linrec_bwd_workspace_bytes(B, T, D, cu_seqlens=None, *, states_given=False,
+                                   gates_precomputed=False) -> int:
+    """Bytes of device workspace gdn_linrec_bwd needs (T: all packed tokens)."""
+    return int(lib.gdn_linrec_bwd_workspace_bytes(
+        _host_offsets(cu_seqlens)[0], B, T, D, int(states_given),
+        GATES_PRECOMPUTED if gates_precomputed else 0))
+
+
+def _workspace(workspace, need, dev):
+    """(tensor to keep, pointer, bytes) of a call's workspace, allocated here when None."""
+    if need == 0:
+        return None, None, 0
+    if workspace is None:
+        workspace = torch.empty(need, device=dev, dtype=torch.uint8)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace: must be contiguous and on {dev}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _linrec_inputs(x, a, b, A_log, dt_bias, gates_precomputed, input_scale):
+    """Checked (arguments, flags) that the recurrence's entry points share."""
+    dt, dev, shape = x.dtype, x.device, x.shape
+    D = shape[-1]
+    if input_scale not in _SCALES:
+        raise ValueError(f"input_scale: expected one of {sorted(_SCALES)}, got {input_scale!r}")
+    gdt = torch.float32 if gates_precomputed else dt
+    px, ldx = _strided(x, dt, shape, dev, "x")
+    pa, lda = _strided(a, gdt, shape, dev, "a")
+    pb, ldb = _strided(b, gdt, shape, dev, "b")
+    pA = pt = None
+    if not gates_precomputed:
+        pA = _dense(A_log, torch.float32, (D,), dev, "A_log")
+        pt = _dense(dt_bias, torch.float32, (D,), dev, "dt_bias")
+    flags = _SCALES[input_scale] | (GATES_PRECOMPUTED if gates_precomputed else 0)
+    return (px, pa, pb, pA, pt), (ldx, lda, ldb), flags
+
+
+def _linrec_sizes(x, cu_seqlens):
+    """(host offsets or None, B, T, D)."""
+    cu, n = _host_offsets(cu_seqlens)
+    if x.dim() != (3 if cu is None else 2):
+        raise ValueError("x: expected [B, T, D], or [T, D] with cu_seqlens")
+    return (cu, n, x.shape[0], x.shape[1]) if cu is not None else (None, *x.shape)
+
+
+@_on_device
+def gdn_linrec_fwd(x, a, b=None, A_log=None, dt_bias=None, h0=None, *, cu_seqlens=None,
+                   input_scale="none", gates_precomputed=False, out_f32=False, h=None, ht=None,
+                   want_ht=True, want_states=False, states=None, workspace=None):
+    """Gated linear recurrence h_t = alpha_t h_{t-1} + s(alpha_t) beta_t x_t per channel, with
+    the delta rules' gates (alpha_t = exp(-exp(A_log) softplus(a_t + dt_bias)), beta_t =
+    sigmoid(b_t), 1 without b) and s = 1, 1 - alpha or sqrt(1 - alpha^2) by input_scale
+    ("none", "tied", "unit").  x, a, b [B,T,D], or [T,D] packed with cu_seqlens (N + 1 token
+    offsets: a list or a CPU int64 tensor); they may be slices of one projection's output.
+    With gates_precomputed a is log alpha and b is beta, float32.  A_log, dt_bias [D], h0 [B,D]
+    float32.  Returns (h, ht), or (h, ht, states) with want_states: the float32 state before
+    each chunk of LINREC_CHUNK tokens [gdn_linrec_chunks(...), D], for gdn_linrec_bwd.  h has
+    the input dtype, or float32 with out_f32, and may be x.  stream: as everywhere."""
+    cu, B, T, D = _linrec_sizes(x, cu_seqlens)
+    ins, lds, flags = _linrec_inputs(x, a, b, A_log, dt_bias, gates_precomputed, input_scale)
+    dev, f32 = x.device, torch.float32
+    odt = f32 if out_f32 else x.dtype
+    if h is None:
+        h = torch.empty(x.shape, device=dev, dtype=odt)
+    ph, ldh = _strided(h, odt, x.shape, dev, "h")
+    if ht is None and want_ht:
+        ht = torch.empty((B, D), device=dev, dtype=f32)
+    if want_states or states is not None:
+        shape = (gdn_linrec_chunks(B, T, cu), D)
+        if states is None:
+            states = torch.empty(shape, device=dev, dtype=f32)
+        want_states = True
+        ps = _dense(states, f32, shape, dev, "states")
+    else:
+        ps = None
+    keep, ws, ws_bytes = _workspace(
+        workspace, lib.gdn_linrec_workspace_bytes(cu, B, T, D), dev)
+    _check(lib.gdn_linrec_fwd(*ins, _dense(h0, f32, (B, D), dev, "h0"), cu, B, T, D, *lds,
+                              _dtype_code(x.dtype), flags | (OUT_F32 if out_f32 else 0), ph, ldh,
+                              _dense(ht, f32, (B, D), dev, "ht"), ps, ws, ws_bytes,
+                              torch.cuda.current_stream().cuda_stream), "gdn_linrec_fwd")
+    return (h, ht, states) if want_states else (h, ht)
+
+
+@_on_device
+def gdn_linrec_bwd(x, a, b, A_log, dt_bias, h0, dh, dht=None, *, cu_seqlens=None,
+                   input_scale="none", gates_precomputed=False, grad_f32=False, states=None,
+                   want_dh0=True, workspace=None):
+    """Gradients of sum(h * dh) + sum(ht * dht) for gdn_linrec_fwd's (h, ht) on the same inputs
+    (see include/gdn.h).  dh in the input dtype (float32 with grad_f32), states: the forward's
+    (None: recomputed here).  Returns a dict: dx, da, db in dh's dtype (da, db float32 with
+    gates_precomputed, with respect to log alpha and beta; db None without b), dA_log,
+    ddt_bias [D] float32 (None with gates_precomputed), dh0 [B,D] float32 (None unless
+    want_dh0).  Tokens behind the last packed sequence get no value."""
+    cu, B, T, D = _linrec_sizes(x, cu_seqlens)
+    ins, lds, flags = _linrec_inputs(x, a, b, A_log, dt_bias, gates_precomputed, input_scale)
+    dev, f32 = x.device, torch.float32
+    ddt = f32 if grad_f32 else x.dtype
+    gdt = f32 if gates_precomputed else ddt
+    pdh, lddh = _strided(dh, ddt, x.shape, dev, "dh")
+    out = {"dx": torch.empty(x.shape, device=dev, dtype=ddt),
+           "da": torch.empty(x.shape, device=dev, dtype=gdt),
+           "db": None if b is None else torch.empty(x.shape, device=dev, dtype=gdt),
+           "dA_log": None, "ddt_bias": None,
+           "dh0": torch.empty((B, D), device=dev, dtype=f32) if want_dh0 else None}
+    if not gates_precomputed:
+        out["dA_log"] = torch.empty((D,), device=dev, dtype=f32)
+        out["ddt_bias"] = torch.empty((D,), device=dev, dtype=f32)
+    ps = None
+    if states is not None:
+        ps = _dense(states, f32, (gdn_linrec_chunks(B, T, cu), D), dev, "states")
+    keep, ws, ws_bytes = _workspace(
+        workspace, lib.gdn_linrec_bwd_workspace_bytes(cu, B, T, D, int(states is not None), flags),
+        dev)
+    ptr = {k: None if v is None else v.data_ptr() for k, v in out.items()}
+    _check(lib.gdn_linrec_bwd(*ins, _dense(h0, f32, (B, D), dev, "h0"), cu, B, T, D, *lds, pdh,
+                              lddh, _dense(dht, f32, (B, D), dev, "dht"), ps,
+                              _dtype_code(x.dtype), flags | (GRAD_F32 if grad_f32 else 0),
+                              ptr["dx"], D, ptr["da"], D, ptr["db"], D, ptr["dA_log"],
+                              ptr["ddt_bias"], ptr["dh0"], ws, ws_bytes,
+                              torch.cuda.current_stream().cuda_stream), "gdn_linrec_bwd")
+    return out
+
+
+@_on_device
+def gdn_linrec_step(x, a, b, A_log, dt_bias, state, *, input_scale="none",
+                    gates_precomputed=False, out_f32=False, h=None):
+    """One token of gdn_linrec_fwd for N sequences: x, a, b [N, D] (b None: beta = 1), state
+    [N, D] float32 updated in place.  Returns h [N, D], which may be x."""
+    if x.dim() != 2:
+        raise ValueError("x: expected [N, D]")
+    N, D = x.shape
+    ins, lds, flags = _linrec_inputs(x, a, b, A_log, dt_bias, gates_precomputed, input_scale)
+    odt = torch.float32 if out_f32 else x.dtype
+    if h is None:
+        h = torch.empty((N, D), device=x.device, dtype=odt)
+    ph, ldh = _strided(h, odt, (N, D), x.device, "h")
+    _check(lib.gdn_linrec_step(*ins, _dense(state, torch.float32, (N, D), x.device, "state"), N,
+                               D, *lds, _dtype_code(x.dtype), flags | (OUT_F32 if out_f32 else 0),
+                               ph, ldh, torch.cuda.current_stream().cuda_stream),
+           "gdn_linrec_step")
+    return h
+
+
+_NORMS = {None: 0, "none": 0, "l2": QK_L2NORM, "rms": QK_RMSNORM}
+
+
+def _rope_inputs(q, k, positions, inv_freq, q_weight, k_weight, norm, interleaved):
+    """Checked arguments that both entry points share."""
+    some = q if q is not None else k
+    dt, dev, lead, d = some.dtype, some.device, some.shape[:-2], some.shape[-1]
+    if len(lead) not in (1, 2):
+        raise ValueError("q, k: expected [T, H, d] or [B, T, H, d]")
+    if norm not in _NORMS:
+        raise ValueError(f"norm: expected 'rms', 'l2' or None, got {norm!r}")
+    Hq, Hk = (0 if t is None else t.shape[-2] for t in (q, k))
+    tokens = lead.numel()
+    pq, ldq = _strided(q, dt, (*lead, Hq, d), dev, "q", 2)
+    pk, ldk = _strided(k, dt, (*lead, Hk, d), dev, "k", 2)
+    rot = 0
+    pp = pf = None
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        pf = _dense(inv_freq, torch.float32, (rot // 2,), dev, "inv_freq")
+        pp = _dense(positions, torch.int64, lead, dev, "positions")
+    pw = [_dense(w, torch.float32, (d,), dev, n)
+          for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight"))]
+    flags = _NORMS[norm] | (ROPE_INTERLEAVED if interleaved else 0)
+    return (pq, pk, pp, pf, *pw, tokens, Hq, Hk, d, rot, ldq, ldk), flags, dt, dev, lead
+
+
+def gdn_qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, *, norm="rms",
+                     eps=1e-6, scale=1.0, interleaved=False, q_out=None, k_out=None,
+                     stream=None):
+    """Norm of every head of q [..., Hq, d] and k [..., Hk, d] ("rms" with the weights [d]
+    float32, "l2", or None) and the rotation of its first 2 * len(inv_freq) channels by
+    positions [...] (int64) * inv_freq (float32; None: no rotation), in one pass; queries are
+    multiplied by scale.  The leading axes are [T] or [B, T]; q and k may be slices of one
+    projection's output, and one of them None.  Returns (q_out, k_out), which may be q and k."""
+    return _rope_fwd(q if q is not None else k, q, k, positions, inv_freq, q_weight, k_weight,
+                     norm, eps, scale, interleaved, q_out, k_out, stream=stream)
+
+
+@_on_device
+def _rope_fwd(_, q, k, positions, inv_freq, q_weight, k_weight, norm, eps, scale, interleaved,
+              q_out, k_out):
+    args, flags, dt, dev, lead = _rope_inputs(q, k, positions, inv_freq, q_weight, k_weight,
+                                              norm, interleaved)
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, device=dev, dtype=dt)
+    if k is not None and k_out is None:
+        k_out = torch.empty(k.shape, device=dev, dtype=dt)
+    po = _strided(q_out, dt, () if q is None else q.shape, dev, "q_out", 2)
+    ko = _strided(k_out, dt, () if k is None else k.shape, dev, "k_out", 2)
+    _check(lib.gdn_qk_norm_rope(*args, _dtype_code(dt), flags, eps, scale, *po, *ko,
+                                torch.cuda.current_stream().cuda_stream), "gdn_qk_norm_rope")
+    return q_out, k_out
+
+
+def gdn_qk_norm_rope_bwd_workspace_bytes(tokens, Hq, Hk, d, norm="rms") -> int:
+    """Bytes of device workspace gdn_qk_norm_rope_bwd needs for the weights' gradients."""
+    return int(lib.gdn_qk_norm_rope_bwd_workspace_bytes(tokens, Hq, Hk, d, _NORMS[norm]))
+
+
+def gdn_qk_norm_rope_bwd(q, k, positions, inv_freq, q_weight, k_weight, dq_out, dk_out, *,
+                         norm="rms", eps=1e-6, scale=1.0, interleaved=False, grad_f32=False,
+                         workspace=None, stream=None):
+    """Gradients of gdn_qk_norm_rope at its inputs q, k and weights, from those at its outputs
+    (the input dtype, or float32 with grad_f32).  Returns a dict: dq, dk in the gradients'
+    dtype, dq_weight, dk_weight [d] float32 (None where the weight is)."""
+    return _rope_bwd(q if q is not None else k, q, k, positions, inv_freq, q_weight, k_weight,
+                     dq_out, dk_out, norm, eps, scale, interleaved, grad_f32, workspace,
+                     stream=stream)
+
+
+@_on_device
+def _rope_bwd(_, q, k, positions, inv_freq, q_weight, k_weight, dq_out, dk_out, norm, eps, scale,
+              interleaved, grad_f32, workspace):
+    args, flags, dt, dev, lead = _rope_inputs(q, k, positions, inv_freq, q_weight, k_weight,
+                                              norm, interleaved)
+    tokens, Hq, Hk, d = args[6:10]
+    gdt = torch.float32 if grad_f32 else dt
+    gq = _strided(dq_out, gdt, () if q is None else q.shape, dev, "dq_out", 2)
+    gk = _strided(dk_out, gdt, () if k is None else k.shape, dev, "dk_out", 2)
+    out = {"dq": None if q is None else torch.empty(q.shape, device=dev, dtype=gdt),
+           "dk": None if k is None else torch.empty(k.shape, device=dev, dtype=gdt)}
+    for name, w in (("dq_weight", q_weight), ("dk_weight", k_weight)):
+        out[name] = None if w is None else torch.empty((d,), device=dev, dtype=torch.float32)
+    need = 0
+    if q_weight is not None or k_weight is not None:
+        need = lib.gdn_qk_norm_rope_bwd_workspace_bytes(tokens, Hq, Hk, d, flags)
+    keep, ws, ws_bytes = _workspace(workspace, need, dev)
+    ptr = {n: None if v is None else v.data_ptr() for n, v in out.items()}
+    _check(lib.gdn_qk_norm_rope_bwd(*args, *gq, *gk, _dtype_code(dt),
+                                    flags | (GRAD_F32 if grad_f32 else 0), eps, scale,
+                                    ptr["dq"], Hq * d, ptr["dk"], Hk * d, ptr["dq_weight"],
+                                    ptr["dk_weight"], ws, ws_bytes,
+                                    torch.cuda.current_stream().cuda_stream),
+           "gdn_qk_norm_rope_bwd")
+    return out
+
+
 def gdn_check_status(stream=None):
     """Synchronise the stream and raise if a bounded device wait expired or an
     fp16 operand left its range since the last check."""
@@ -627,5 +992,5 @@ def gdn_status(stream=None) -> int:
 def gdn_test_set_wait_fault(site: int, spin_limit: int = 0):
     """Test hook: make the tensor-core chunk kernels leave one bounded wait to
     expire (site 1: the scan's first state hand-off, site 2: the prep's K / Q
-    tiles; 0: none), with spin_limit polls per wait (0 = the default)."""
+    tiles, site 3: the chunk states of the linear recurrence; 0: none), with spin_limit polls per wait (0 = the default)."""
     _check(lib.gdn_test_set_wait_fault(int(site), int(spin_limit)), "gdn_test_set_wait_fault")

@@ -10,6 +10,7 @@
 #include "chunk_layout.cuh"
 #include "common.cuh"
 #include "launch.h"
+#include "linrec.cuh"
 
 namespace gdn {
 
@@ -509,10 +510,218 @@ int gdn_check_status(gdn_stream_t stream) {
 }
 
 int gdn_test_set_wait_fault(int site, unsigned spin_limit) {
-  if (site < kFaultNone || site > kFaultPrepTiles) return GDN_ERR_INVALID_ARG;
+  if (site < kFaultNone || site > kFaultLinrec) return GDN_ERR_INVALID_ARG;
   g_fault_site.store(site);
   g_fault_spin.store(spin_limit == 0 ? kWaitSpin : spin_limit);
   return GDN_OK;
+}
+
+// ---- gated linear recurrence ------------------------------------------------------------
+
+// The checks the recurrence's calls share; *chunks is set where they pass.
+static int validate_linrec(const LinrecArgs& p, int more_flags, long long* chunks) {
+  const int scales = GDN_LINREC_TIED | GDN_LINREC_UNIT;
+  if (p.B < 0 || p.T < 0 || p.D <= 0 || !ok_dtype(p.dtype)) return GDN_ERR_INVALID_ARG;
+  if (p.flags & ~(GDN_GATES_PRECOMPUTED | scales | more_flags)) return GDN_ERR_INVALID_ARG;
+  if ((p.flags & scales) == scales) return GDN_ERR_INVALID_ARG;
+  if (p.cu != nullptr) {
+    if (p.cu[0] != 0 || p.cu[p.B] > p.T) return GDN_ERR_INVALID_ARG;
+    for (int i = 0; i < p.B; ++i)
+      if (p.cu[i + 1] < p.cu[i]) return GDN_ERR_INVALID_ARG;
+  }
+  *chunks = linrec_chunks(p.cu, p.B, p.T);
+  // chunk and tile numbers are 32-bit
+  if (*chunks * ((p.D + 31) / 32) > 0x3fffffffLL) return GDN_ERR_UNSUPPORTED;
+  if (p.B == 0 || *chunks == 0) return GDN_OK;
+  const size_t es = elem_size(p.dtype), ges = (p.flags & GDN_GATES_PRECOMPUTED) ? 4 : es;
+  if (!ok_elem(p.x, es) || !ok_elem(p.a, ges) || (p.b != nullptr && !ok_elem(p.b, ges)))
+    return GDN_ERR_INVALID_ARG;
+  if (p.ldx < p.D || p.lda < p.D || (p.b != nullptr && p.ldb < p.D)) return GDN_ERR_INVALID_ARG;
+  if (!(p.flags & GDN_GATES_PRECOMPUTED) && (!ok_elem(p.A_log, 4) || !ok_elem(p.dt_bias, 4)))
+    return GDN_ERR_INVALID_ARG;
+  return GDN_OK;
+}
+static bool ok_opt_f32(const void* p) { return p == nullptr || ok_elem(p, 4); }
+static bool ok_workspace(const void* ws, size_t ws_bytes, size_t need) {
+  return need == 0 || (ok_ptr(ws) && ws_bytes >= need);
+}
+static bool ok_sizes(const long long* cu, int B, int T, int D) {
+  if (B <= 0 || T < 0 || D <= 0) return false;
+  for (int i = 0; cu != nullptr && i < B; ++i)
+    if (cu[i + 1] < cu[i]) return false;
+  return true;
+}
+
+size_t gdn_linrec_workspace_bytes(const long long* cu_seqlens, int B, int T, int D) {
+  return ok_sizes(cu_seqlens, B, T, D) ? linrec_workspace_bytes(cu_seqlens, B, T, D) : 0;
+}
+size_t gdn_linrec_bwd_workspace_bytes(const long long* cu_seqlens, int B, int T, int D,
+                                      int states_given, int flags) {
+  return ok_sizes(cu_seqlens, B, T, D)
+             ? linrec_bwd_workspace_bytes(cu_seqlens, B, T, D, states_given != 0, flags)
+             : 0;
+}
+
+int gdn_linrec_fwd(const void* x, const void* a, const void* b, const float* A_log,
+                   const float* dt_bias, const float* h0, const long long* cu_seqlens, int B,
+                   int T, int D, long long ldx, long long lda, long long ldb, int dtype,
+                   int flags, void* h, long long ldh, float* ht, float* states,
+                   void* workspace, size_t ws_bytes, gdn_stream_t stream) {
+  LinrecArgs p{};
+  p.x = x; p.a = a; p.b = b; p.A_log = A_log; p.dt_bias = dt_bias; p.h0 = h0;
+  p.cu = cu_seqlens; p.B = B; p.T = T; p.D = D; p.ldx = ldx; p.lda = lda; p.ldb = ldb;
+  p.dtype = dtype; p.flags = flags; p.h = h; p.ldh = ldh; p.ht = ht; p.states_out = states;
+  long long chunks = 0;
+  const int st = validate_linrec(p, GDN_OUT_F32, &chunks);
+  if (st != GDN_OK) return st;
+  if (!ok_opt_f32(h0) || !ok_opt_f32(ht) || !ok_opt_f32(states)) return GDN_ERR_INVALID_ARG;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (B == 0) return GDN_OK;
+  if (chunks == 0) return from_cuda(launch_copy_state(h0, ht, (size_t)B * D, s));
+  if (!ok_elem(h, (flags & GDN_OUT_F32) ? 4 : elem_size(dtype)) || ldh < D)
+    return GDN_ERR_INVALID_ARG;
+  if (!ok_workspace(workspace, ws_bytes, linrec_workspace_bytes(cu_seqlens, B, T, D)))
+    return GDN_ERR_WORKSPACE;
+  return from_cuda(launch_linrec_fwd(p, workspace, s));
+}
+
+int gdn_linrec_bwd(const void* x, const void* a, const void* b, const float* A_log,
+                   const float* dt_bias, const float* h0, const long long* cu_seqlens, int B,
+                   int T, int D, long long ldx, long long lda, long long ldb, const void* dh,
+                   long long lddh, const float* dht, const float* states, int dtype, int flags,
+                   void* dx, long long lddx, void* da, long long ldda, void* db, long long lddb,
+                   float* dA_log, float* ddt_bias, float* dh0, void* workspace,
+                   size_t ws_bytes, gdn_stream_t stream) {
+  LinrecArgs p{};
+  p.x = x; p.a = a; p.b = b; p.A_log = A_log; p.dt_bias = dt_bias; p.h0 = h0;
+  p.cu = cu_seqlens; p.B = B; p.T = T; p.D = D; p.ldx = ldx; p.lda = lda; p.ldb = ldb;
+  p.dtype = dtype; p.flags = flags; p.dh = dh; p.lddh = lddh; p.dht = dht; p.states = states;
+  p.dx = dx; p.lddx = lddx; p.da = da; p.ldda = ldda; p.db = db; p.lddb = lddb;
+  p.dA_log = dA_log; p.ddt_bias = ddt_bias; p.dh0 = dh0;
+  long long chunks = 0;
+  const int st = validate_linrec(p, GDN_GRAD_F32, &chunks);
+  if (st != GDN_OK) return st;
+  const bool given = flags & GDN_GATES_PRECOMPUTED;
+  if (!ok_opt_f32(h0) || !ok_opt_f32(dht) || !ok_opt_f32(dh0) || !ok_opt_f32(states))
+    return GDN_ERR_INVALID_ARG;
+  if (!given && (!ok_elem(dA_log, 4) || !ok_elem(ddt_bias, 4))) return GDN_ERR_INVALID_ARG;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (B == 0 || chunks == 0) {
+    cudaError_t e = launch_copy_state(dht, dh0, (size_t)B * D, s);
+    if (e == cudaSuccess && !given) e = launch_copy_state(nullptr, dA_log, D, s);
+    if (e == cudaSuccess && !given) e = launch_copy_state(nullptr, ddt_bias, D, s);
+    return from_cuda(e);
+  }
+  const size_t es = elem_size(dtype), ds = (flags & GDN_GRAD_F32) ? 4 : es, gs = given ? 4 : ds;
+  if ((b == nullptr) != (db == nullptr)) return GDN_ERR_INVALID_ARG;
+  if (!ok_elem(dh, ds) || lddh < D || !ok_elem(dx, ds) || lddx < D || !ok_elem(da, gs) ||
+      ldda < D || (db != nullptr && (!ok_elem(db, gs) || lddb < D)))
+    return GDN_ERR_INVALID_ARG;
+  if (!ok_workspace(workspace, ws_bytes,
+                    linrec_bwd_workspace_bytes(cu_seqlens, B, T, D, states != nullptr, flags)))
+    return GDN_ERR_WORKSPACE;
+  return from_cuda(launch_linrec_bwd(p, workspace, s));
+}
+
+int gdn_linrec_step(const void* x, const void* a, const void* b, const float* A_log,
+                    const float* dt_bias, float* state, int N, int D, long long ldx,
+                    long long lda, long long ldb, int dtype, int flags, void* h, long long ldh,
+                    gdn_stream_t stream) {
+  LinrecArgs p{};
+  p.x = x; p.a = a; p.b = b; p.A_log = A_log; p.dt_bias = dt_bias;
+  p.B = N; p.T = 1; p.D = D; p.ldx = ldx; p.lda = lda; p.ldb = ldb;
+  p.dtype = dtype; p.flags = flags; p.h = h; p.ldh = ldh;
+  long long chunks = 0;
+  const int st = validate_linrec(p, GDN_OUT_F32, &chunks);
+  if (st != GDN_OK || N == 0) return st;
+  if (!ok_elem(state, 4) || !ok_elem(h, (flags & GDN_OUT_F32) ? 4 : elem_size(dtype)) || ldh < D)
+    return GDN_ERR_INVALID_ARG;
+  return from_cuda(launch_linrec_step(p, state, (cudaStream_t)stream));
+}
+
+// ---- norm and rotation of q and k ---------------------------------------------------------
+
+static int validate_rope(const QkRopeArgs& p, int more_flags) {
+  const int norms = GDN_QK_L2NORM | GDN_QK_RMSNORM;
+  if (p.tokens < 0 || p.Hq < 0 || p.Hk < 0 || p.d <= 0 || !ok_dtype(p.dtype))
+    return GDN_ERR_INVALID_ARG;
+  if (p.flags & ~(norms | GDN_ROPE_INTERLEAVED | more_flags)) return GDN_ERR_INVALID_ARG;
+  if ((p.flags & norms) == norms || p.rot < 0 || p.rot % 2 != 0 || p.rot > p.d)
+    return GDN_ERR_INVALID_ARG;
+  if (!(p.eps >= 0.f) || p.eps > 1.f) return GDN_ERR_INVALID_ARG;
+  if (!(p.flags & GDN_QK_RMSNORM) && (p.q_weight || p.k_weight || p.dqw || p.dkw))
+    return GDN_ERR_INVALID_ARG;
+  if (!ok_opt_f32(p.q_weight) || !ok_opt_f32(p.k_weight) || !ok_opt_f32(p.dqw) ||
+      !ok_opt_f32(p.dkw))
+    return GDN_ERR_INVALID_ARG;
+  if (p.d > 256 || p.Hq + (long long)p.Hk > (1 << 20) || p.tokens > (1LL << 40))
+    return GDN_ERR_UNSUPPORTED;
+  if (p.tokens == 0 || p.Hq + p.Hk == 0) return GDN_OK;
+  const size_t es = elem_size(p.dtype);
+  if (p.rot > 0 && (!ok_elem(p.positions, 8) || !ok_elem(p.inv_freq, 4)))
+    return GDN_ERR_INVALID_ARG;
+  if (p.Hq > 0 && (!ok_elem(p.q, es) || p.ldq < (long long)p.Hq * p.d)) return GDN_ERR_INVALID_ARG;
+  if (p.Hk > 0 && (!ok_elem(p.k, es) || p.ldk < (long long)p.Hk * p.d)) return GDN_ERR_INVALID_ARG;
+  const size_t os = (p.flags & GDN_GRAD_F32) ? 4 : es;
+  if (p.Hq > 0 && (!ok_elem(p.q_out, os) || p.ldqo < (long long)p.Hq * p.d))
+    return GDN_ERR_INVALID_ARG;
+  if (p.Hk > 0 && (!ok_elem(p.k_out, os) || p.ldko < (long long)p.Hk * p.d))
+    return GDN_ERR_INVALID_ARG;
+  return GDN_OK;
+}
+
+int gdn_qk_norm_rope(const void* q, const void* k, const long long* positions,
+                     const float* inv_freq, const float* q_weight, const float* k_weight,
+                     long long tokens, int Hq, int Hk, int d, int rot, long long ldq,
+                     long long ldk, int dtype, int flags, float eps, float scale, void* q_out,
+                     long long ldqo, void* k_out, long long ldko, gdn_stream_t stream) {
+  QkRopeArgs p{};
+  p.q = q; p.k = k; p.positions = positions; p.inv_freq = inv_freq;
+  p.q_weight = q_weight; p.k_weight = k_weight;
+  p.tokens = tokens; p.Hq = Hq; p.Hk = Hk; p.d = d; p.rot = rot; p.dtype = dtype;
+  p.flags = flags; p.ldq = ldq; p.ldk = ldk; p.eps = eps; p.scale = scale;
+  p.q_out = q_out; p.k_out = k_out; p.ldqo = ldqo; p.ldko = ldko;
+  const int st = validate_rope(p, 0);
+  if (st != GDN_OK || tokens == 0 || Hq + Hk == 0) return st;
+  return from_cuda(launch_qk_rope(p, (cudaStream_t)stream));
+}
+
+size_t gdn_qk_norm_rope_bwd_workspace_bytes(long long tokens, int Hq, int Hk, int d, int flags) {
+  if (tokens <= 0 || Hq < 0 || Hk < 0 || Hq + (long long)Hk == 0 || d <= 0 || d > 256) return 0;
+  return qk_rope_bwd_workspace_bytes(tokens, Hq, Hk, d, flags);
+}
+
+int gdn_qk_norm_rope_bwd(const void* q, const void* k, const long long* positions,
+                         const float* inv_freq, const float* q_weight, const float* k_weight,
+                         long long tokens, int Hq, int Hk, int d, int rot, long long ldq,
+                         long long ldk, const void* dq_out, long long lddqo, const void* dk_out,
+                         long long lddko, int dtype, int flags, float eps, float scale, void* dq,
+                         long long lddq, void* dk, long long lddk, float* dq_weight,
+                         float* dk_weight, void* workspace, size_t ws_bytes,
+                         gdn_stream_t stream) {
+  QkRopeArgs p{};
+  p.q = q; p.k = k; p.positions = positions; p.inv_freq = inv_freq;
+  p.q_weight = q_weight; p.k_weight = k_weight;
+  p.tokens = tokens; p.Hq = Hq; p.Hk = Hk; p.d = d; p.rot = rot; p.dtype = dtype;
+  p.flags = flags; p.ldq = ldq; p.ldk = ldk; p.eps = eps; p.scale = scale;
+  p.gq = dq_out; p.gk = dk_out; p.ldgq = lddqo; p.ldgk = lddko;
+  p.q_out = dq; p.k_out = dk; p.ldqo = lddq; p.ldko = lddk;
+  p.dqw = dq_weight; p.dkw = dk_weight;
+  const int st = validate_rope(p, GDN_GRAD_F32);
+  if (st != GDN_OK) return st;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (tokens == 0 || Hq + Hk == 0) {  // sums over nothing
+    cudaError_t e = launch_copy_state(nullptr, dq_weight, d, s);
+    if (e == cudaSuccess) e = launch_copy_state(nullptr, dk_weight, d, s);
+    return from_cuda(e);
+  }
+  const size_t gs = (flags & GDN_GRAD_F32) ? 4 : elem_size(dtype);
+  if (Hq > 0 && (!ok_elem(dq_out, gs) || lddqo < (long long)Hq * d)) return GDN_ERR_INVALID_ARG;
+  if (Hk > 0 && (!ok_elem(dk_out, gs) || lddko < (long long)Hk * d)) return GDN_ERR_INVALID_ARG;
+  if ((dq_weight || dk_weight) &&
+      !ok_workspace(workspace, ws_bytes, qk_rope_bwd_workspace_bytes(tokens, Hq, Hk, d, flags)))
+    return GDN_ERR_WORKSPACE;
+  return from_cuda(launch_qk_rope_bwd(p, workspace, s));
 }
 
 }  // extern "C"

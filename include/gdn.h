@@ -82,6 +82,20 @@ enum {
   GDN_OUT_F32 = 4            /* o is written as float32 whatever `dtype` is      */
 };
 
+/* Flags of the gated linear recurrence and of the norm-and-rotation of q and k. */
+enum {
+  GDN_LINREC_TIED = 8,       /* input scale 1 - alpha                            */
+  GDN_LINREC_UNIT = 16,      /* input scale sqrt(1 - alpha^2)                    */
+  GDN_GRAD_F32 = 32,         /* backward: the gradients that are read per token
+                                and written per token are float32 whatever
+                                `dtype` is                                       */
+  GDN_QK_RMSNORM = 64,       /* norm x / sqrt(mean(x^2) + eps) * weight          */
+  GDN_ROPE_INTERLEAVED = 128 /* pairs are channels (2i, 2i + 1), not (i, i + rot/2) */
+};
+
+/* Tokens of a chunk of the gated linear recurrence (rows of its `states`). */
+#define GDN_LINREC_CHUNK 64
+
 /*
  * gdn_gate_prep -- the gate and L2-norm prologue as one elementwise kernel.
  * ("Qwen3.5", module skeleton: beta = sigmoid(b), g = -exp(A_log) *
@@ -454,6 +468,153 @@ int gdn2_chunk_fwd(const void* q, const void* k, const void* v, const void* a,
 size_t gdn2_chunk_workspace_bytes(int B, int T, int H, int dk, int dv, int dtype);
 
 /*
+ * gdn_linrec_fwd -- the gated linear recurrence, a vector state next to the matrix
+ * states above: per channel c of D
+ *    g_t = -exp(A_log) softplus(a_t + dt_bias),  alpha_t = e^{g_t},
+ *    beta_t = sigmoid(b_t),
+ *    h_t = alpha_t h_{t-1} + s(alpha_t) beta_t x_t,
+ * with s = 1, or 1 - alpha (GDN_LINREC_TIED), or sqrt(1 - alpha^2)
+ * (GDN_LINREC_UNIT).  The gates are those of the delta rules ("从 Full Attention 到
+ * Gated DeltaNet" section 9), one per channel; the rule without keys is
+ * S_t = alpha_t S_{t-1} + (input) of the pages' gated linear attention ("Qwen3.5",
+ * GDN详解) with a vector in the place of the matrix.
+ *   x, a, b    [B, T, D], or [T, D] packed with cu_seqlens: dtype, read; b NULL: beta = 1.
+ *              ldx, lda, ldb: elements from one token to the next (>= D; the rows of a
+ *              batch follow one another, T * ld apart), so that slices of a fused
+ *              projection are read where they are.
+ *              With GDN_GATES_PRECOMPUTED a holds g (<= 0) and b holds beta, float32.
+ *   A_log,
+ *   dt_bias    [D] float32 (unused with GDN_GATES_PRECOMPUTED)
+ *   h0         [B, D] float32, read; NULL = zeros
+ *   cu_seqlens NULL, or a HOST array of B + 1 int64, the sequences' first tokens as for
+ *              gdn_chunk_fwd_varlen, cu_seqlens[B] <= T.  Tokens behind the last
+ *              sequence are not read and their outputs are left as they were.
+ *   h          [B, T, D] or [T, D] dtype (float32 with GDN_OUT_F32), ldh elements from
+ *              token to token, written; may be x itself (same type and ldh = ldx),
+ *              and must not overlap any other input
+ *   ht         [B, D] float32, written; NULL = not stored; may be h0
+ *   states     [chunks, D] float32, written; NULL = not stored: the state before each
+ *              chunk of GDN_LINREC_CHUNK tokens of a sequence (the sequences' chunks one
+ *              after another, ceil(length / GDN_LINREC_CHUNK) each), for gdn_linrec_bwd
+ *   flags      GDN_GATES_PRECOMPUTED, GDN_OUT_F32, GDN_LINREC_TIED or GDN_LINREC_UNIT
+ *   workspace / ws_bytes: device scratch owned by the caller, 16-byte aligned, at least
+ *              gdn_linrec_workspace_bytes() bytes, overwritten -> else GDN_ERR_WORKSPACE.
+ *              Calls that may run at the same time need a workspace each.
+ *   Every pointer needs its element alignment only (rows that are 16-byte aligned move
+ *   in 16-byte pieces).  States and sums are float32, outputs rounded once; the result
+ *   does not depend on how the work was scheduled.  T = 0 and empty sequences copy h0
+ *   to ht (or zeros).  The kernels wait for one another's chunk states, with a limit:
+ *   an expired wait is reported by gdn_check_status.
+ */
+int gdn_linrec_fwd(const void* x, const void* a, const void* b, const float* A_log,
+                   const float* dt_bias, const float* h0, const long long* cu_seqlens, int B,
+                   int T, int D, long long ldx, long long lda, long long ldb, int dtype,
+                   int flags, void* h, long long ldh, float* ht, float* states,
+                   void* workspace, size_t ws_bytes, gdn_stream_t stream);
+
+/* Device workspace bytes gdn_linrec_fwd needs (0 for invalid sizes). */
+size_t gdn_linrec_workspace_bytes(const long long* cu_seqlens, int B, int T, int D);
+
+/*
+ * gdn_linrec_bwd -- the backward of gdn_linrec_fwd: the gradients of sum(h * dh) +
+ * sum(ht * dht).  With c the gradient that arrives from later tokens (c = dht behind the
+ * last one): lambda_t = dh_t + c_t, c_{t-1} = alpha_t lambda_t, and
+ *    dx = lambda s beta,  dbeta = lambda s x,
+ *    dg = alpha lambda h_{t-1} + lambda beta x ds/dg.
+ * h is recomputed in float32 from `states`, so the rounding of a bf16 h does not reach
+ * the gradients.
+ *   x ... ldb, dtype: as given to the forward, read (GDN_OUT_F32 does not apply)
+ *   dh     [B, T, D] or [T, D] dtype (float32 with GDN_GRAD_F32), lddh as above, read
+ *   dht    [B, D] float32, read; NULL = zeros
+ *   states the forward's, read; NULL: recomputed into the workspace (reads x, a, b again)
+ *   dx, da, db [B, T, D] or [T, D] dtype (float32 with GDN_GRAD_F32; da and db always
+ *     float32 with GDN_GATES_PRECOMPUTED, where they are the gradients at g and beta),
+ *     written; db NULL exactly when b is; they must not overlap the inputs or each other
+ *   dA_log, ddt_bias [D] float32, written (sums over all tokens, in a fixed order);
+ *     unused with GDN_GATES_PRECOMPUTED
+ *   dh0    [B, D] float32, written; NULL = not stored; may be dht
+ *   flags      GDN_GATES_PRECOMPUTED, GDN_GRAD_F32, GDN_LINREC_TIED or GDN_LINREC_UNIT
+ *   workspace / ws_bytes: as above, sized by gdn_linrec_bwd_workspace_bytes.
+ * Tokens behind the last packed sequence are left as they were.
+ */
+int gdn_linrec_bwd(const void* x, const void* a, const void* b, const float* A_log,
+                   const float* dt_bias, const float* h0, const long long* cu_seqlens, int B,
+                   int T, int D, long long ldx, long long lda, long long ldb, const void* dh,
+                   long long lddh, const float* dht, const float* states, int dtype, int flags,
+                   void* dx, long long lddx, void* da, long long ldda, void* db, long long lddb,
+                   float* dA_log, float* ddt_bias, float* dh0, void* workspace,
+                   size_t ws_bytes, gdn_stream_t stream);
+
+/* Device workspace bytes gdn_linrec_bwd needs; states_given: the call passes `states`. */
+size_t gdn_linrec_bwd_workspace_bytes(const long long* cu_seqlens, int B, int T, int D,
+                                      int states_given, int flags);
+
+/*
+ * gdn_linrec_step -- one token of the gated linear recurrence for N sequences: the decode
+ * step beside gdn_recurrent_step, the same gates and input scale as gdn_linrec_fwd.
+ *   x, a, b [N, D] dtype (a, b float32 g, beta with GDN_GATES_PRECOMPUTED; b NULL: beta
+ *     = 1), ldx, lda, ldb elements from one sequence to the next
+ *   state   [N, D] float32, read and updated in place
+ *   h       [N, D] dtype (float32 with GDN_OUT_F32), ldh, written; may be x
+ *   flags   as for gdn_linrec_fwd
+ */
+int gdn_linrec_step(const void* x, const void* a, const void* b, const float* A_log,
+                    const float* dt_bias, float* state, int N, int D, long long ldx,
+                    long long lda, long long ldb, int dtype, int flags, void* h, long long ldh,
+                    gdn_stream_t stream);
+
+/*
+ * gdn_qk_norm_rope -- norm of every head of q and k and the rotation by position, in one
+ * pass (what the attention layers of the hybrid stack run on q and k: "Qwen3.5"
+ * (rainlin-net), the full-attention module with its q and k norms and rotary embedding;
+ * with GDN_QK_L2NORM, the delta rules' own norm with positions):
+ *    n = x / sqrt(mean(x^2) + eps) * weight   (GDN_QK_RMSNORM), or
+ *    n = x / sqrt(sum(x^2) + eps)             (GDN_QK_L2NORM), or n = x (neither),
+ *    (p, q) -> (p cos - q sin, q cos + p sin), angle = position * inv_freq[i],
+ * over the pairs i of the first rot channels: channels (i, i + rot/2), or (2i, 2i + 1)
+ * with GDN_ROPE_INTERLEAVED; the other channels pass through.  Queries are multiplied by
+ * scale after that.
+ *   q [tokens, Hq, d], k [tokens, Hk, d] dtype, read; heads dense, ldq, ldk elements from
+ *     token to token (>= H * d).  Hq or Hk may be 0 (its pointers unused).
+ *   positions [tokens] int64 device, any value (the angle is exact for all of them: turns
+ *     are 64-bit fractions); inv_freq [rot/2] float32 device; both unused with rot = 0
+ *   q_weight, k_weight [d] float32, or NULL = ones; only with GDN_QK_RMSNORM
+ *   d from 1 to 256, rot even, 0 <= rot <= d, 0 <= eps <= 1
+ *   q_out, k_out: dtype, ldqo, ldko; written; may be q, k (same ld), must not otherwise
+ *     overlap an input
+ * float32 arithmetic, outputs rounded once.  Element alignment is enough.
+ */
+int gdn_qk_norm_rope(const void* q, const void* k, const long long* positions,
+                     const float* inv_freq, const float* q_weight, const float* k_weight,
+                     long long tokens, int Hq, int Hk, int d, int rot, long long ldq,
+                     long long ldk, int dtype, int flags, float eps, float scale, void* q_out,
+                     long long ldqo, void* k_out, long long ldko, gdn_stream_t stream);
+
+/*
+ * gdn_qk_norm_rope_bwd -- its backward: from the gradients at q_out and k_out, those at q,
+ * k and the weights.
+ *   q ... scale: as given to the forward (q, k its inputs, not its outputs), read
+ *   dq_out, dk_out: dtype (float32 with GDN_GRAD_F32), lddqo, lddko, read
+ *   dq, dk: the same type, lddq, lddk, written; may be dq_out, dk_out (same ld), and must
+ *     not otherwise overlap an input
+ *   dq_weight, dk_weight [d] float32, written (summed over tokens and heads in a fixed
+ *     order); NULL = not wanted; only with GDN_QK_RMSNORM
+ *   workspace / ws_bytes: device scratch, 16-byte aligned, at least
+ *     gdn_qk_norm_rope_bwd_workspace_bytes() bytes where a weight's gradient is wanted.
+ */
+int gdn_qk_norm_rope_bwd(const void* q, const void* k, const long long* positions,
+                         const float* inv_freq, const float* q_weight, const float* k_weight,
+                         long long tokens, int Hq, int Hk, int d, int rot, long long ldq,
+                         long long ldk, const void* dq_out, long long lddqo, const void* dk_out,
+                         long long lddko, int dtype, int flags, float eps, float scale, void* dq,
+                         long long lddq, void* dk, long long lddk, float* dq_weight,
+                         float* dk_weight, void* workspace, size_t ws_bytes,
+                         gdn_stream_t stream);
+
+/* Device workspace bytes gdn_qk_norm_rope_bwd needs (0 without GDN_QK_RMSNORM). */
+size_t gdn_qk_norm_rope_bwd_workspace_bytes(long long tokens, int Hq, int Hk, int d, int flags);
+
+/*
  * gdn_check_status -- waits for `stream`, then reads and clears the device
  * status word of the current device.  Returns GDN_OK, GDN_ERR_TIMEOUT if a
  * bounded wait in a kernel expired since the last check (reported first when
@@ -475,7 +636,9 @@ int gdn_check_status(gdn_stream_t stream);
  *   site 0: no fault (the default);
  *   site 1: the state scan issues no first products, so its epilogue's wait for
  *           them expires;
- *   site 2: the WY prep withholds its K / Q tile loads.
+ *   site 2: the WY prep withholds its K / Q tile loads;
+ *   site 3: the linear recurrence's first chunks do not publish their states, so the
+ *           waits of the chunks after them expire.
  *   spin_limit: polls before a wait gives up, for every bounded wait of those
  *   kernels (0 = the default, 2^24).  The setting is process-wide and stays
  *   until changed; the outputs of a faulted call are not valid.
