@@ -1,9 +1,9 @@
-// linrec.cu -- the gated linear recurrence, per channel
-//   h_t = alpha_t h_{t-1} + f(alpha_t) beta_t x_t
-// (linrec_math.cuh for the gates), over dense or packed batches, its backward and its
-// one-token step.  One thread per (sequence, channel) walks the tokens in order.
-#include "linrec.cuh"
-#include "linrec_math.cuh"
+// linrec.cu -- the scan of the gated linear recurrence,
+//   h_t = alpha_t h_{t-1} + f(alpha_t) beta_t x_t  per channel
+// (linrec_math.cuh for the gates, linrec_chain.cuh for the split along time), and its
+// one-token step.  Host side of the scan and of the backward (linrec_bwd.cu).
+#include "linrec_chain.cuh"
+#include "linrec_launch.cuh"
 
 namespace gdn {
 
@@ -16,15 +16,158 @@ long long linrec_chunks(const long long* cu, int B, int T) {
 
 namespace {
 
-constexpr int kT = 128;
-
-size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
-
-// Packed batches: each sequence's first token and first chunk, entry B the totals.
-struct SeqTab {
-  const long long* cu;
-  const int* chunk0;
+template <typename TX, typename TG>
+struct FwdStage {
+  alignas(16) TX x[kTileT * kTileC];
+  alignas(16) TG a[kTileT * kTileC];
+  alignas(16) TG b[kTileT * kTileC];
 };
+template <typename TX, typename TG>
+struct FwdSmem {
+  FwdStage<TX, TG> stage[2];
+  float4 fold[kWorkWarps][32];  // (A, H) of each warp's tokens
+  float2 in[32];                // what enters the tile
+  Tile tile[3];                 // this tile's, the next one's, the one after
+  int more[3];
+};
+
+template <typename TX, typename TG, bool GIVEN, int SCALE, typename TO>
+__global__ void __launch_bounds__(kLinrecThreads)
+linrec_fwd_kernel(LinrecArgs p, Chain ch, int vec) {
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  auto& sm = *reinterpret_cast<FwdSmem<TX, TG>*>(smem_raw);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const bool work = warp < kWorkWarps;
+  const bool pair = vec & 8;
+  if (threadIdx.x == kWorkThreads) {
+    next_tile<false>(ch, sm, 0);
+    next_tile<false>(ch, sm, 1);
+  }
+  __syncthreads();
+  auto load = [&](int k) {
+    if (sm.more[k % 3]) {
+      const Tile& t = sm.tile[k % 3];
+      FwdStage<TX, TG>& st = sm.stage[k & 1];
+      load_tile(st.x, p.x, p.ldx, t, p.D, vec & 1);
+      load_tile(st.a, p.a, p.lda, t, p.D, vec & 2);
+      if (p.b) load_tile(st.b, p.b, p.ldb, t, p.D, vec & 4);
+    }
+    cp_async_commit();
+  };
+  if (work) load(0);
+  GateConst k0{0.f, 0.f}, k1{0.f, 0.f};
+  int c0 = -1;
+  for (int k = 0;; ++k) {
+    cp_async_wait<0>();
+    __syncthreads();  // the stage is complete, the other one free, the tiles' numbers known
+    if (!sm.more[k % 3]) return;
+    const Tile t = sm.tile[k % 3];
+    const int c = t.c0 + 2 * lane;
+    float al[kPer][2], u[kPer][2];
+    if (work) {
+      load(k + 1);
+      if (!GIVEN && c0 != t.c0) {
+        c0 = t.c0;
+        if (c < p.D) k0 = gate_const(p.A_log, p.dt_bias, c);
+        if (c + 1 < p.D) k1 = gate_const(p.A_log, p.dt_bias, c + 1);
+      }
+      const FwdStage<TX, TG>& st = sm.stage[k & 1];
+      float A0 = 1.f, A1 = 1.f, H0 = 0.f, H1 = 0.f;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int at = (warp * kPer + i) * kTileC + 2 * lane;
+        const float2 av = get2(st.a + at), xv = get2(st.x + at);
+        const float g0 = log_decay<GIVEN>(av.x, k0), g1 = log_decay<GIVEN>(av.y, k1);
+        al[i][0] = ex2_f(g0 * kLog2e);
+        al[i][1] = ex2_f(g1 * kLog2e);
+        u[i][0] = xv.x * input_scale<SCALE>(g0);
+        u[i][1] = xv.y * input_scale<SCALE>(g1);
+        if (p.b) {
+          const float2 bv = get2(st.b + at);
+          u[i][0] *= write_gate<GIVEN>(bv.x);
+          u[i][1] *= write_gate<GIVEN>(bv.y);
+        }
+      }
+      if (t.n < kTileT) {  // behind the sequence: the state passes through
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          if (warp * kPer + i >= t.n) {
+            al[i][0] = al[i][1] = 1.f;
+            u[i][0] = u[i][1] = 0.f;
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        H0 = fmaf(al[i][0], H0, u[i][0]);
+        H1 = fmaf(al[i][1], H1, u[i][1]);
+        A0 *= al[i][0];
+        A1 *= al[i][1];
+      }
+      sm.fold[warp][lane] = make_float4(A0, H0, A1, H1);
+    } else if (lane == 0) {
+      next_tile<false>(ch, sm, k + 2);
+    }
+    __syncthreads();
+    float4 ex = make_float4(1.f, 0.f, 1.f, 0.f);  // what the tile's tokens before do
+    if (work) {
+      if (p.h) {
+        for (int w = 0; w < warp; ++w) {
+          const float4 f = sm.fold[w][lane];
+          ex.y = fmaf(f.x, ex.y, f.y);
+          ex.w = fmaf(f.z, ex.w, f.w);
+          ex.x *= f.x;
+          ex.z *= f.z;
+        }
+      }
+    } else {
+      float4 own = make_float4(1.f, 0.f, 1.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWorkWarps; ++w) {
+        const float4 f = sm.fold[w][lane];
+        own.y = fmaf(f.x, own.y, f.y);
+        own.w = fmaf(f.z, own.w, f.w);
+        own.x *= f.x;
+        own.z *= f.z;
+      }
+      const float2 in = chain_in<1>(ch, t, own, p.h0 ? p.h0 + (long long)t.row * p.D : nullptr);
+      sm.in[lane] = in;
+      const float2 out = make_float2(fmaf(own.x, in.x, own.y), fmaf(own.z, in.y, own.w));
+      if (t.before == 0 && p.states_out) write2(p.states_out + (long long)t.chunk * p.D, c, p.D, in);
+      if (t.after > 0) chain_out<1>(ch, t, out);
+      else if (p.ht) write2(p.ht + (long long)t.row * p.D, c, p.D, out);
+    }
+    __syncthreads();
+    if (work && p.h) {
+      const float2 in = sm.in[lane];
+      float h0 = fmaf(ex.x, in.x, ex.y), h1 = fmaf(ex.z, in.y, ex.w);
+      TO* out = static_cast<TO*>(p.h) + (t.tok + warp * kPer) * p.ldh + c;
+      const int cols = p.D - c;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        h0 = fmaf(al[i][0], h0, u[i][0]);
+        h1 = fmaf(al[i][1], h1, u[i][1]);
+        if (warp * kPer + i < t.n) put2(out, h0, h1, cols < 2 ? cols : 2, pair);
+        out += p.ldh;
+      }
+    }
+  }
+}
+
+template <typename TX, typename TG, bool GIVEN, int SCALE, typename TO>
+__global__ void __launch_bounds__(128) linrec_step_kernel(LinrecArgs p, float* state) {
+  const int blocks = (p.D + 127) / 128;
+  const long long r = blockIdx.x / blocks;
+  const int c = (blockIdx.x % blocks) * 128 + threadIdx.x;
+  if (c >= p.D) return;
+  const GateConst k = GIVEN ? GateConst{0.f, 0.f} : gate_const(p.A_log, p.dt_bias, c);
+  const float g = log_decay<GIVEN>(to_f32(static_cast<const TG*>(p.a)[r * p.lda + c]), k);
+  float u = to_f32(static_cast<const TX*>(p.x)[r * p.ldx + c]) * input_scale<SCALE>(g);
+  if (p.b) u *= write_gate<GIVEN>(to_f32(static_cast<const TG*>(p.b)[r * p.ldb + c]));
+  const float st = fmaf(ex2_f(g * kLog2e), state[r * p.D + c], u);
+  state[r * p.D + c] = st;
+  static_cast<TO*>(p.h)[r * p.ldh + c] = from_f32<TO>(st);
+}
+
 constexpr int kPiece = 240;  // entries of a table piece passed by value (< 4 KB of arguments)
 struct TabPiece {
   long long cu[kPiece];
@@ -37,13 +180,7 @@ __global__ void seq_table_kernel(TabPiece p, long long* cu, int* chunk0) {
     chunk0[p.first + i] = p.chunk0[i];
   }
 }
-size_t seq_table_bytes(int B) {
-  return align256((size_t)(B + 1) * sizeof(long long)) + align256((size_t)(B + 1) * sizeof(int));
-}
-cudaError_t fill_seq_table(const long long* cu, int B, void* at, SeqTab* tab, cudaStream_t s) {
-  long long* dcu = static_cast<long long*>(at);
-  int* dch = reinterpret_cast<int*>(static_cast<char*>(at) +
-                                    align256((size_t)(B + 1) * sizeof(long long)));
+cudaError_t fill_seq_table(const long long* cu, int B, const SeqTab& tab, cudaStream_t s) {
   long long chunks = 0;
   TabPiece p;
   for (int i0 = 0; i0 <= B; i0 += kPiece) {
@@ -55,182 +192,33 @@ cudaError_t fill_seq_table(const long long* cu, int B, void* at, SeqTab* tab, cu
       p.chunk0[i] = (int)chunks;
       if (j < B) chunks += (cu[j + 1] - cu[j] + kLinrecChunk - 1) / kLinrecChunk;
     }
-    seq_table_kernel<<<1, 256, 0, s>>>(p, dcu, dch);
+    seq_table_kernel<<<1, 256, 0, s>>>(p, const_cast<long long*>(tab.cu),
+                                       const_cast<int*>(tab.chunk0));
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  tab->cu = dcu;
-  tab->chunk0 = dch;
   return cudaSuccess;
 }
 
-template <typename TX, typename TG, bool GIVEN, int SCALE, typename TO>
-__global__ void __launch_bounds__(kT)
-linrec_fwd_kernel(LinrecArgs p, SeqTab tab, float* states) {
-  const int c = blockIdx.x * kT + threadIdx.x, r = blockIdx.y;
-  if (c >= p.D) return;
-  const bool packed = tab.cu != nullptr;
-  const long long t0 = packed ? tab.cu[r] : (long long)r * p.T;
-  const int n = packed ? (int)(tab.cu[r + 1] - t0) : p.T;
-  const long long chunk0 =
-      packed ? tab.chunk0[r] : (long long)r * ((p.T + kLinrecChunk - 1) / kLinrecChunk);
-  const TX* x = static_cast<const TX*>(p.x) + t0 * p.ldx + c;
-  const TG* a = static_cast<const TG*>(p.a) + t0 * p.lda + c;
-  const TG* b = p.b ? static_cast<const TG*>(p.b) + t0 * p.ldb + c : nullptr;
-  TO* h = p.h ? static_cast<TO*>(p.h) + t0 * p.ldh + c : nullptr;
-  const GateConst k = GIVEN ? GateConst{0.f, 0.f} : gate_const(p.A_log, p.dt_bias, c);
-  float st = p.h0 ? p.h0[(size_t)r * p.D + c] : 0.f;
-  for (int t = 0; t < n; ++t) {
-    if (states != nullptr && t % kLinrecChunk == 0)
-      states[(chunk0 + t / kLinrecChunk) * p.D + c] = st;
-    const float g = log_decay<GIVEN>(to_f32(a[t * p.lda]), k);
-    float u = to_f32(x[t * p.ldx]) * input_scale<SCALE>(g);
-    if (b) u *= write_gate<GIVEN>(to_f32(b[t * p.ldb]));
-    st = fmaf(ex2_f(g * kLog2e), st, u);
-    if (h) h[t * p.ldh] = from_f32<TO>(st);
-  }
-  if (p.ht) p.ht[(size_t)r * p.D + c] = st;
+// What an empty sequence's chain starts with is what it ends with.
+__global__ void copy_empty_kernel(const long long* cu, int D, const float* src, float* dst) {
+  const int r = blockIdx.x;
+  if (cu[r + 1] != cu[r]) return;
+  for (int c = threadIdx.x; c < D; c += blockDim.x)
+    dst[(long long)r * D + c] = src ? src[(long long)r * D + c] : 0.f;
 }
-
-template <typename TX, typename TG, bool GIVEN, int SCALE, typename TD, typename TDG>
-__global__ void __launch_bounds__(kT)
-linrec_bwd_kernel(LinrecArgs p, SeqTab tab, const float* states, float2* sums) {
-  const int c = blockIdx.x * kT + threadIdx.x, r = blockIdx.y;
-  if (c >= p.D) return;
-  const bool packed = tab.cu != nullptr;
-  const long long t0 = packed ? tab.cu[r] : (long long)r * p.T;
-  const int n = packed ? (int)(tab.cu[r + 1] - t0) : p.T;
-  const long long chunk0 =
-      packed ? tab.chunk0[r] : (long long)r * ((p.T + kLinrecChunk - 1) / kLinrecChunk);
-  const TX* x = static_cast<const TX*>(p.x) + t0 * p.ldx + c;
-  const TG* a = static_cast<const TG*>(p.a) + t0 * p.lda + c;
-  const TG* b = p.b ? static_cast<const TG*>(p.b) + t0 * p.ldb + c : nullptr;
-  const TD* dh = static_cast<const TD*>(p.dh) + t0 * p.lddh + c;
-  TD* dx = static_cast<TD*>(p.dx) + t0 * p.lddx + c;
-  TDG* da = static_cast<TDG*>(p.da) + t0 * p.ldda + c;
-  TDG* db = b ? static_cast<TDG*>(p.db) + t0 * p.lddb + c : nullptr;
-  const GateConst k = GIVEN ? GateConst{0.f, 0.f} : gate_const(p.A_log, p.dt_bias, c);
-  float carry = p.dht ? p.dht[(size_t)r * p.D + c] : 0.f;
-  double sum_A = 0.0, sum_b = 0.0;
-  float prev[kLinrecChunk];
-  for (int j = (n + kLinrecChunk - 1) / kLinrecChunk - 1; j >= 0; --j) {
-    const int lo = j * kLinrecChunk, m = n - lo < kLinrecChunk ? n - lo : kLinrecChunk;
-    float st = states[(chunk0 + j) * p.D + c];
-    for (int i = 0; i < m; ++i) {
-      prev[i] = st;
-      const float g = log_decay<GIVEN>(to_f32(a[(lo + i) * p.lda]), k);
-      float u = to_f32(x[(lo + i) * p.ldx]) * input_scale<SCALE>(g);
-      if (b) u *= write_gate<GIVEN>(to_f32(b[(lo + i) * p.ldb]));
-      st = fmaf(ex2_f(g * kLog2e), st, u);
-    }
-    for (int i = m - 1; i >= 0; --i) {
-      const int t = lo + i;
-      const float av = to_f32(a[t * p.lda]), xv = to_f32(x[t * p.ldx]);
-      const float g = log_decay<GIVEN>(av, k), alpha = ex2_f(g * kLog2e);
-      const float f = input_scale<SCALE>(g);
-      const float beta = b ? write_gate<GIVEN>(to_f32(b[t * p.ldb])) : 1.f;
-      const float lam = to_f32(dh[t * p.lddh]) + carry;
-      carry = alpha * lam;
-      const float dg = fmaf(carry, prev[i], lam * xv * beta * input_scale_slope<SCALE>(alpha, f));
-      dx[t * p.lddx] = from_f32<TD>(lam * f * beta);
-      if (b) {
-        const float dbeta = lam * f * xv;
-        db[t * p.lddb] =
-            from_f32<TDG>(GIVEN ? dbeta : dbeta * beta * sigmoid_sfu(-to_f32(b[t * p.ldb])));
-      }
-      if (GIVEN) {
-        da[t * p.ldda] = from_f32<TDG>(dg);
-      } else {
-        const float dz = dg * k.neg_A * sigmoid_sfu(av + k.bias);
-        da[t * p.ldda] = from_f32<TDG>(dz);
-        sum_b += dz;
-        sum_A += dg == 0.f ? 0.f : dg * g;  // g = -inf where alpha = 0
-      }
-    }
-  }
-  if (p.dh0) p.dh0[(size_t)r * p.D + c] = carry;
-  if (!GIVEN) sums[(size_t)r * p.D + c] = make_float2((float)sum_A, (float)sum_b);
-}
-
-__global__ void linrec_sums_kernel(const float2* sums, long long rows, int D, float* dA_log,
-                                   float* ddt_bias) {
-  const int c = blockIdx.x * blockDim.x + threadIdx.x;
-  if (c >= D) return;
-  double A = 0.0, b = 0.0;
-  for (long long r = 0; r < rows; ++r) {
-    const float2 v = sums[r * D + c];
-    A += v.x;
-    b += v.y;
-  }
-  dA_log[c] = (float)A;
-  ddt_bias[c] = (float)b;
-}
-
-template <typename TX, typename TG, bool GIVEN, int SCALE, typename TO>
-__global__ void __launch_bounds__(kT) linrec_step_kernel(LinrecArgs p, float* state) {
-  const int c = blockIdx.x * kT + threadIdx.x;
-  const long long r = blockIdx.y;
-  if (c >= p.D) return;
-  const GateConst k = GIVEN ? GateConst{0.f, 0.f} : gate_const(p.A_log, p.dt_bias, c);
-  const float g = log_decay<GIVEN>(to_f32(static_cast<const TG*>(p.a)[r * p.lda + c]), k);
-  float u = to_f32(static_cast<const TX*>(p.x)[r * p.ldx + c]) * input_scale<SCALE>(g);
-  if (p.b) u *= write_gate<GIVEN>(to_f32(static_cast<const TG*>(p.b)[r * p.ldb + c]));
-  const float st = fmaf(ex2_f(g * kLog2e), state[r * p.D + c], u);
-  state[r * p.D + c] = st;
-  static_cast<TO*>(p.h)[r * p.ldh + c] = from_f32<TO>(st);
-}
-
-// Calls f.template run<TX, TG, GIVEN, SCALE, wide>() for the call's types: x in TX, the
-// gates in TG, `wide`: the outputs (forward) or gradients (backward) in float32.
-template <typename F, typename TX, typename TG, bool GIVEN, bool WIDE>
-cudaError_t by_scale(const LinrecArgs& p, F f) {
-  if (p.flags & GDN_LINREC_TIED) return f.template run<TX, TG, GIVEN, kScaleTied, WIDE>();
-  if (p.flags & GDN_LINREC_UNIT) return f.template run<TX, TG, GIVEN, kScaleUnit, WIDE>();
-  return f.template run<TX, TG, GIVEN, kScaleNone, WIDE>();
-}
-template <typename F>
-cudaError_t by_type(const LinrecArgs& p, int wide_flag, F f) {
-  using bf16 = __nv_bfloat16;
-  const bool given = p.flags & GDN_GATES_PRECOMPUTED;
-  if (p.dtype == GDN_F32)
-    return given ? by_scale<F, float, float, true, true>(p, f)
-                 : by_scale<F, float, float, false, true>(p, f);
-  if (p.flags & wide_flag)
-    return given ? by_scale<F, bf16, float, true, true>(p, f)
-                 : by_scale<F, bf16, bf16, false, true>(p, f);
-  return given ? by_scale<F, bf16, float, true, false>(p, f)
-               : by_scale<F, bf16, bf16, false, false>(p, f);
-}
-template <typename TX, bool WIDE> struct Wide { using type = TX; };
-template <typename TX> struct Wide<TX, true> { using type = float; };
 
 struct FwdRun {
   const LinrecArgs& p;
-  SeqTab tab;
-  float* states;
+  const Chain& ch;
   cudaStream_t s;
   template <typename TX, typename TG, bool GIVEN, int SCALE, bool WIDE>
-  cudaError_t run() {
-    linrec_fwd_kernel<TX, TG, GIVEN, SCALE, typename Wide<TX, WIDE>::type>
-        <<<dim3((p.D + kT - 1) / kT, p.B), kT, 0, s>>>(p, tab, states);
-    return cudaGetLastError();
-  }
-};
-struct BwdRun {
-  const LinrecArgs& p;
-  SeqTab tab;
-  const float* states;
-  float2* sums;
-  cudaStream_t s;
-  template <typename TX, typename TG, bool GIVEN, int SCALE, bool WIDE>
-  cudaError_t run() {
-    using TD = typename Wide<TX, WIDE>::type;
-    linrec_bwd_kernel<TX, TG, GIVEN, SCALE, TD, typename Wide<TD, GIVEN>::type>
-        <<<dim3((p.D + kT - 1) / kT, p.B), kT, 0, s>>>(p, tab, states, sums);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || GIVEN) return e;
-    linrec_sums_kernel<<<(p.D + 127) / 128, 128, 0, s>>>(sums, p.B, p.D, p.dA_log, p.ddt_bias);
-    return cudaGetLastError();
+  cudaError_t run() const {
+    using TO = typename Wide<TX, WIDE>::type;
+    const int vec = rows16(p.x, p.ldx, sizeof(TX)) | rows16(p.a, p.lda, sizeof(TG)) << 1 |
+                    rows16(p.b, p.ldb, sizeof(TG)) << 2 | pairs(p.h, p.ldh, sizeof(TO)) << 3;
+    return launch_chain(linrec_fwd_kernel<TX, TG, GIVEN, SCALE, TO>, sizeof(FwdSmem<TX, TG>), p,
+                        ch, vec, s);
   }
 };
 struct StepRun {
@@ -238,56 +226,81 @@ struct StepRun {
   float* state;
   cudaStream_t s;
   template <typename TX, typename TG, bool GIVEN, int SCALE, bool WIDE>
-  cudaError_t run() {
+  cudaError_t run() const {
+    const long long blocks = (long long)p.B * ((p.D + 127) / 128);
     linrec_step_kernel<TX, TG, GIVEN, SCALE, typename Wide<TX, WIDE>::type>
-        <<<dim3((p.D + kT - 1) / kT, p.B), kT, 0, s>>>(p, state);
+        <<<(unsigned)blocks, 128, 0, s>>>(p, state);
     return cudaGetLastError();
   }
 };
 
+bool any_neighbours(const LinrecArgs& a) {
+  if (a.cu == nullptr) return a.T > kLinrecChunk;
+  for (int i = 0; i < a.B; ++i)
+    if (a.cu[i + 1] - a.cu[i] > kLinrecChunk) return true;
+  return false;
+}
+
 }  // namespace
 
+// Workspace: the sequence table; the ticket and a flag a tile; the tiles' aggregates; the
+// chunks' carries.
 size_t linrec_workspace_bytes(const long long* cu, int B, int T, int D) {
-  return cu ? seq_table_bytes(B) : 0;
+  return chain_bytes(cu, B, T, D);
 }
-size_t linrec_bwd_workspace_bytes(const long long* cu, int B, int T, int D, bool states_given,
-                                  int flags) {
-  size_t n = cu ? seq_table_bytes(B) : 0;
-  if (!states_given) n += align256((size_t)linrec_chunks(cu, B, T) * D * sizeof(float));
-  if (!(flags & GDN_GATES_PRECOMPUTED)) n += align256((size_t)B * D * sizeof(float2));
-  return n;
+
+cudaError_t make_chain(const LinrecArgs& a, void* workspace, float* carry, bool table,
+                       cudaStream_t s, Chain* ch) {
+  char* ws = static_cast<char*>(workspace);
+  const long long chunks = linrec_chunks(a.cu, a.B, a.T);
+  ch->B = a.B; ch->T = a.T; ch->D = a.D;
+  ch->nblk = (a.D + kTileC - 1) / kTileC;
+  ch->per_row = (int)(((long long)a.T + kTileT - 1) / kTileT);
+  ch->tiles = (int)(chunks * ch->nblk);
+  if (a.cu) {
+    ch->tab.cu = reinterpret_cast<const long long*>(ws);
+    ch->tab.chunk0 =
+        reinterpret_cast<const int*>(ws + align256((size_t)(a.B + 1) * sizeof(long long)));
+    if (table) {
+      cudaError_t e = fill_seq_table(a.cu, a.B, ch->tab, s);
+      if (e != cudaSuccess) return e;
+    }
+    ws += seq_table_bytes(a.B);
+  }
+  const size_t flag_bytes = flags_bytes(ch->tiles);
+  ch->ticket = any_neighbours(a) ? reinterpret_cast<int*>(ws) : nullptr;
+  ch->flags = reinterpret_cast<int*>(ws) + 64;
+  ch->agg = reinterpret_cast<float4*>(ws + flag_bytes);
+  ch->carry = carry ? carry
+                    : reinterpret_cast<float*>(ws + flag_bytes + (size_t)ch->tiles * 32 * sizeof(float4));
+  ch->status = status_word();
+  if (ch->status == nullptr) return cudaErrorUnknown;
+  const WaitFault wf = wait_fault();
+  ch->spin = wf.spin < kLinrecSpin ? wf.spin : kLinrecSpin;
+  ch->fault = wf.site == kFaultLinrec;
+  return ch->ticket ? cudaMemsetAsync(ws, 0, flag_bytes, s) : cudaSuccess;
+}
+
+cudaError_t copy_empty(const LinrecArgs& a, const Chain& ch, const float* src, float* dst,
+                       cudaStream_t s) {
+  if (a.cu == nullptr || dst == nullptr || src == dst) return cudaSuccess;
+  bool any = false;
+  for (int i = 0; i < a.B; ++i) any |= a.cu[i + 1] == a.cu[i];
+  if (!any) return cudaSuccess;
+  copy_empty_kernel<<<a.B, 128, 0, s>>>(ch.tab.cu, a.D, src, dst);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_linrec_scan(const LinrecArgs& a, const Chain& ch, int wide_flag,
+                               cudaStream_t s) {
+  return by_type(a, wide_flag, FwdRun{a, ch, s});
 }
 
 cudaError_t launch_linrec_fwd(const LinrecArgs& a, void* workspace, cudaStream_t s) {
-  SeqTab tab{nullptr, nullptr};
-  if (a.cu) {
-    cudaError_t e = fill_seq_table(a.cu, a.B, workspace, &tab, s);
-    if (e != cudaSuccess) return e;
-  }
-  return by_type(a, GDN_OUT_F32, FwdRun{a, tab, a.states_out, s});
-}
-
-cudaError_t launch_linrec_bwd(const LinrecArgs& a, void* workspace, cudaStream_t s) {
-  SeqTab tab{nullptr, nullptr};
-  char* ws = static_cast<char*>(workspace);
-  if (a.cu) {
-    cudaError_t e = fill_seq_table(a.cu, a.B, ws, &tab, s);
-    if (e != cudaSuccess) return e;
-    ws += seq_table_bytes(a.B);
-  }
-  const float* states = a.states;
-  if (states == nullptr) {
-    float* own = reinterpret_cast<float*>(ws);
-    ws += align256((size_t)linrec_chunks(a.cu, a.B, a.T) * a.D * sizeof(float));
-    LinrecArgs f = a;
-    f.h = nullptr;
-    f.ht = nullptr;
-    cudaError_t e = by_type(f, GDN_GRAD_F32, FwdRun{f, tab, own, s});
-    if (e != cudaSuccess) return e;
-    states = own;
-  }
-  return by_type(a, GDN_GRAD_F32,
-                 BwdRun{a, tab, states, reinterpret_cast<float2*>(ws), s});
+  Chain ch{};
+  cudaError_t e = make_chain(a, workspace, a.states_out, true, s, &ch);
+  if (e == cudaSuccess) e = launch_linrec_scan(a, ch, GDN_OUT_F32, s);
+  return e != cudaSuccess ? e : copy_empty(a, ch, a.h0, a.ht, s);
 }
 
 cudaError_t launch_linrec_step(const LinrecArgs& a, float* state, cudaStream_t s) {

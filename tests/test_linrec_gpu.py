@@ -400,3 +400,24 @@ def test_refused_tensors():
         G.gdn_linrec_fwd(d["x"].half(), d["a"].half(), None, *ok[3:])
     with pytest.raises(ValueError):
         G.gdn_linrec_bwd(*ok, d["dh"], d["dht"], states=torch.zeros(1, 16, device="cuda"))
+
+
+def test_an_expired_wait_is_reported():
+    """The first chunks keep their states to themselves: the waits behind them end and say so,
+    and the next call is right again."""
+    _, d = make(2, 300, 70, F32, seed=16)
+    h, ht, st = G.gdn_linrec_fwd(*ins(d), want_states=True)
+    g = G.gdn_linrec_bwd(*ins(d), d["dh"], d["dht"], states=st)
+    torch.cuda.synchronize()
+    try:
+        G.gdn_test_set_wait_fault(3, 1 << 10)
+        G.gdn_linrec_fwd(*ins(d))
+        assert G.gdn_status() == -4
+        G.gdn_linrec_bwd(*ins(d), d["dh"], d["dht"], states=st)
+        assert G.gdn_status() == -4
+    finally:
+        G.gdn_test_set_wait_fault(0, 0)
+    h2, ht2 = G.gdn_linrec_fwd(*ins(d))
+    g2 = G.gdn_linrec_bwd(*ins(d), d["dh"], d["dht"], states=st)
+    assert torch.equal(h, h2) and torch.equal(ht, ht2)
+    assert all(torch.equal(g[k], g2[k]) for k in g)
