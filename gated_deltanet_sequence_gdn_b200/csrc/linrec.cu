@@ -1,8 +1,7 @@
 // linrec.cu -- the scan of the gated linear recurrence,
 //   h_t = alpha_t h_{t-1} + f(alpha_t) beta_t x_t  per channel
-// (linrec_math.cuh for the gates, linrec_chain.cuh for the split along time), and its
+// (linrec_math.cuh for the gates, linrec_tile.cuh for the split along time), and its
 // one-token step.  Host side of the scan and of the backward (linrec_bwd.cu).
-#include "linrec_chain.cuh"
 #include "linrec_launch.cuh"
 
 namespace gdn {
@@ -25,147 +24,128 @@ struct FwdStage {
 template <typename TX, typename TG>
 struct FwdSmem {
   FwdStage<TX, TG> stage[2];
-  float4 fold[kWorkWarps][32];  // (A, H) of each warp's tokens
-  float2 in[32];                // what enters the tile
-  Tile tile[3];                 // this tile's, the next one's, the one after
-  int more[3];
+  CarrySmem carry;
 };
 
 template <typename TX, typename TG, bool GIVEN, int SCALE, typename TO>
-__global__ void __launch_bounds__(kLinrecThreads)
-linrec_fwd_kernel(LinrecArgs p, Chain ch, int vec) {
+__global__ void __launch_bounds__(kLinrecThreads, sizeof(TX) + sizeof(TG) == 4 ? 4 : 2)
+linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   auto& sm = *reinterpret_cast<FwdSmem<TX, TG>*>(smem_raw);
+  FoldRow* folds = reinterpret_cast<FoldRow*>(smem_raw + sizeof(FwdSmem<TX, TG>));
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-  const bool work = warp < kWorkWarps;
-  const bool pair = vec & 8;
-  if (threadIdx.x == kWorkThreads) {
-    next_tile<false>(ch, sm, 0);
-    next_tile<false>(ch, sm, 1);
-  }
-  __syncthreads();
-  auto load = [&](int k) {
-    if (sm.more[k % 3]) {
-      const Tile& t = sm.tile[k % 3];
-      FwdStage<TX, TG>& st = sm.stage[k & 1];
-      load_tile(st.x, p.x, p.ldx, t, p.D, vec & 1);
-      load_tile(st.a, p.a, p.lda, t, p.D, vec & 2);
-      if (p.b) load_tile(st.b, p.b, p.ldb, t, p.D, vec & 4);
+  const Chain k = chain_of(p, ch);
+  const int c = k.c0 + 2 * lane, cols = p.D - c;
+  auto load = [&](int round) {
+    const int tt = round * ch.cs + k.rank;
+    if (tt < k.chunks) {
+      const long long left = k.len - (long long)tt * kTileT, tok = k.tok + (long long)tt * kTileT;
+      const int n = left < kTileT ? (int)left : kTileT;
+      FwdStage<TX, TG>& st = sm.stage[round & 1];
+      load_tile(st.x, p.x, p.ldx, tok, n, k.c0, p.D, vec & 1);
+      load_tile(st.a, p.a, p.lda, tok, n, k.c0, p.D, vec & 2);
+      if (p.b) load_tile(st.b, p.b, p.ldb, tok, n, k.c0, p.D, vec & 4);
     }
     cp_async_commit();
   };
-  if (work) load(0);
-  GateConst k0{0.f, 0.f}, k1{0.f, 0.f};
-  int c0 = -1;
-  for (int k = 0;; ++k) {
+  load(0);
+  carry_begin(ch, sm.carry);
+  GateConst gc{both(0.f), both(0.f)};
+  if (!GIVEN) gc = gate_const(p.A_log, p.dt_bias, c, p.D);
+  float2 carry = read2(p.h0, k.row, c, p.D);  // before the round's first tile (warp 0's)
+  bool lost = false;
+  const int rounds = (k.chunks + ch.cs - 1) / ch.cs;
+  for (int round = 0; round < rounds; ++round) {
     cp_async_wait<0>();
-    __syncthreads();  // the stage is complete, the other one free, the tiles' numbers known
-    if (!sm.more[k % 3]) return;
-    const Tile t = sm.tile[k % 3];
-    const int c = t.c0 + 2 * lane;
-    float al[kPer][2], u[kPer][2];
-    if (work) {
-      load(k + 1);
-      if (!GIVEN && c0 != t.c0) {
-        c0 = t.c0;
-        if (c < p.D) k0 = gate_const(p.A_log, p.dt_bias, c);
-        if (c + 1 < p.D) k1 = gate_const(p.A_log, p.dt_bias, c + 1);
-      }
-      const FwdStage<TX, TG>& st = sm.stage[k & 1];
-      float A0 = 1.f, A1 = 1.f, H0 = 0.f, H1 = 0.f;
+    __syncthreads();  // the stage is complete, the other one free
+    if (round + 1 < rounds) load(round + 1);
+    const int tt = round * ch.cs + k.rank;
+    const long long left = k.len - (long long)tt * kTileT;
+    const int n = left < kTileT ? (left < 0 ? 0 : (int)left) : kTileT;
+    const FwdStage<TX, TG>& st = sm.stage[round & 1];
+    float2 al[kPer], u[kPer];
+    float2 A = both(1.f), H = both(0.f);
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int at = (warp * kPer + i) * kTileC + 2 * lane;
-        const float2 av = get2(st.a + at), xv = get2(st.x + at);
-        const float g0 = log_decay<GIVEN>(av.x, k0), g1 = log_decay<GIVEN>(av.y, k1);
-        al[i][0] = ex2_f(g0 * kLog2e);
-        al[i][1] = ex2_f(g1 * kLog2e);
-        u[i][0] = xv.x * input_scale<SCALE>(g0);
-        u[i][1] = xv.y * input_scale<SCALE>(g1);
-        if (p.b) {
-          const float2 bv = get2(st.b + at);
-          u[i][0] *= write_gate<GIVEN>(bv.x);
-          u[i][1] *= write_gate<GIVEN>(bv.y);
-        }
-      }
-      if (t.n < kTileT) {  // behind the sequence: the state passes through
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-          if (warp * kPer + i >= t.n) {
-            al[i][0] = al[i][1] = 1.f;
-            u[i][0] = u[i][1] = 0.f;
-          }
-      }
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        H0 = fmaf(al[i][0], H0, u[i][0]);
-        H1 = fmaf(al[i][1], H1, u[i][1]);
-        A0 *= al[i][0];
-        A1 *= al[i][1];
-      }
-      sm.fold[warp][lane] = make_float4(A0, H0, A1, H1);
-    } else if (lane == 0) {
-      next_tile<false>(ch, sm, k + 2);
+    for (int i = 0; i < kPer; ++i) {
+      const int at = (warp * kPer + i) * kTileC + 2 * lane;
+      const float2 e = decay_exponent<GIVEN>(get2(st.a + at), gc);
+      al[i] = ex2_2(e);
+      u[i] = get2(st.x + at);
+      if (SCALE != kScaleNone) u[i] = mul2(u[i], input_scale<SCALE>(e, al[i]));
+      if (p.b) u[i] = mul2(u[i], write_gate<GIVEN>(get2(st.b + at)));
     }
-    __syncthreads();
-    float4 ex = make_float4(1.f, 0.f, 1.f, 0.f);  // what the tile's tokens before do
-    if (work) {
-      if (p.h) {
-        for (int w = 0; w < warp; ++w) {
-          const float4 f = sm.fold[w][lane];
-          ex.y = fmaf(f.x, ex.y, f.y);
-          ex.w = fmaf(f.z, ex.w, f.w);
-          ex.x *= f.x;
-          ex.z *= f.z;
+    if (n < kTileT) {  // behind the sequence: the state passes through
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (warp * kPer + i >= n) {
+          al[i] = both(1.f);
+          u[i] = both(0.f);
         }
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      H = fma2(al[i], H, u[i]);
+      A = mul2(A, al[i]);
+    }
+    sm.carry.fold[warp][lane] = join4(A, H);
+    __syncthreads();
+    A = both(1.f);  // what the tile's tokens before the warp's do
+    H = both(0.f);
+    if (warp == 0) {
+      float2 tA = both(1.f), tH = both(0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float4 f = sm.carry.fold[w][lane];
+        tH = fma2(first2(f), tH, last2(f));
+        tA = mul2(tA, first2(f));
       }
+      const float2 in = carry_round(ch, k.rank, round, join4(tA, tH), sm.carry, folds, &carry, &lost);
+      sm.carry.in[lane] = in;
+      if (n > 0) write2(p.states_out, k.chunk0 + tt, c, p.D, in);
     } else {
-      float4 own = make_float4(1.f, 0.f, 1.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kWorkWarps; ++w) {
-        const float4 f = sm.fold[w][lane];
-        own.y = fmaf(f.x, own.y, f.y);
-        own.w = fmaf(f.z, own.w, f.w);
-        own.x *= f.x;
-        own.z *= f.z;
+      for (int w = 0; w < warp; ++w) {
+        const float4 f = sm.carry.fold[w][lane];
+        H = fma2(first2(f), H, last2(f));
+        A = mul2(A, first2(f));
       }
-      const float2 in = chain_in<1>(ch, t, own, p.h0 ? p.h0 + (long long)t.row * p.D : nullptr);
-      sm.in[lane] = in;
-      const float2 out = make_float2(fmaf(own.x, in.x, own.y), fmaf(own.z, in.y, own.w));
-      if (t.before == 0 && p.states_out) write2(p.states_out + (long long)t.chunk * p.D, c, p.D, in);
-      if (t.after > 0) chain_out<1>(ch, t, out);
-      else if (p.ht) write2(p.ht + (long long)t.row * p.D, c, p.D, out);
     }
     __syncthreads();
-    if (work && p.h) {
-      const float2 in = sm.in[lane];
-      float h0 = fmaf(ex.x, in.x, ex.y), h1 = fmaf(ex.z, in.y, ex.w);
-      TO* out = static_cast<TO*>(p.h) + (t.tok + warp * kPer) * p.ldh + c;
-      const int cols = p.D - c;
+    if (p.h) {
+      float2 h = fma2(A, sm.carry.in[lane], H);
+      TO* out = static_cast<TO*>(p.h) + (k.tok + (long long)tt * kTileT + warp * kPer) * p.ldh + c;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        h0 = fmaf(al[i][0], h0, u[i][0]);
-        h1 = fmaf(al[i][1], h1, u[i][1]);
-        if (warp * kPer + i < t.n) put2(out, h0, h1, cols < 2 ? cols : 2, pair);
+        h = fma2(al[i], h, u[i]);
+        if (warp * kPer + i < n) put2(out, h, cols, vec & 8);
         out += p.ldh;
       }
     }
   }
+  if (k.rank == 0 && warp == 0) write2(p.ht, k.row, c, p.D, carry);
+  carry_end(ch);
 }
 
+// Two channels from anywhere a row has them.
+template <typename T>
+__device__ __forceinline__ float2 take2(const void* base, long long at, int cols) {
+  const T* p = static_cast<const T*>(base) + at;
+  return make_float2(to_f32(p[0]), cols > 1 ? to_f32(p[1]) : 0.f);
+}
 template <typename TX, typename TG, bool GIVEN, int SCALE, typename TO>
 __global__ void __launch_bounds__(128) linrec_step_kernel(LinrecArgs p, float* state) {
-  const int blocks = (p.D + 127) / 128;
+  const int blocks = (p.D + 255) / 256;
   const long long r = blockIdx.x / blocks;
-  const int c = (blockIdx.x % blocks) * 128 + threadIdx.x;
-  if (c >= p.D) return;
-  const GateConst k = GIVEN ? GateConst{0.f, 0.f} : gate_const(p.A_log, p.dt_bias, c);
-  const float g = log_decay<GIVEN>(to_f32(static_cast<const TG*>(p.a)[r * p.lda + c]), k);
-  float u = to_f32(static_cast<const TX*>(p.x)[r * p.ldx + c]) * input_scale<SCALE>(g);
-  if (p.b) u *= write_gate<GIVEN>(to_f32(static_cast<const TG*>(p.b)[r * p.ldb + c]));
-  const float st = fmaf(ex2_f(g * kLog2e), state[r * p.D + c], u);
-  state[r * p.D + c] = st;
-  static_cast<TO*>(p.h)[r * p.ldh + c] = from_f32<TO>(st);
+  const int c = (blockIdx.x % blocks) * 256 + 2 * threadIdx.x, cols = p.D - c;
+  if (cols <= 0) return;
+  GateConst gc{both(0.f), both(0.f)};
+  if (!GIVEN) gc = gate_const(p.A_log, p.dt_bias, c, p.D);
+  const float2 e = decay_exponent<GIVEN>(take2<TG>(p.a, r * p.lda + c, cols), gc);
+  const float2 al = ex2_2(e);
+  float2 u = mul2(take2<TX>(p.x, r * p.ldx + c, cols), input_scale<SCALE>(e, al));
+  if (p.b) u = mul2(u, write_gate<GIVEN>(take2<TG>(p.b, r * p.ldb + c, cols)));
+  const float2 st = fma2(al, read2(state, r, c, p.D), u);
+  write2(state, r, c, p.D, st);
+  put2(static_cast<TO*>(p.h) + r * p.ldh + c, st, cols, false);
 }
 
 constexpr int kPiece = 240;  // entries of a table piece passed by value (< 4 KB of arguments)
@@ -200,25 +180,18 @@ cudaError_t fill_seq_table(const long long* cu, int B, const SeqTab& tab, cudaSt
   return cudaSuccess;
 }
 
-// What an empty sequence's chain starts with is what it ends with.
-__global__ void copy_empty_kernel(const long long* cu, int D, const float* src, float* dst) {
-  const int r = blockIdx.x;
-  if (cu[r + 1] != cu[r]) return;
-  for (int c = threadIdx.x; c < D; c += blockDim.x)
-    dst[(long long)r * D + c] = src ? src[(long long)r * D + c] : 0.f;
-}
-
 struct FwdRun {
   const LinrecArgs& p;
-  const Chain& ch;
+  const Chains& ch;
   cudaStream_t s;
   template <typename TX, typename TG, bool GIVEN, int SCALE, bool WIDE>
   cudaError_t run() const {
     using TO = typename Wide<TX, WIDE>::type;
     const int vec = rows16(p.x, p.ldx, sizeof(TX)) | rows16(p.a, p.lda, sizeof(TG)) << 1 |
                     rows16(p.b, p.ldb, sizeof(TG)) << 2 | pairs(p.h, p.ldh, sizeof(TO)) << 3;
-    return launch_chain(linrec_fwd_kernel<TX, TG, GIVEN, SCALE, TO>, sizeof(FwdSmem<TX, TG>), p,
-                        ch, vec, s);
+    int cs = 1;
+    return launch_chains(linrec_fwd_kernel<TX, TG, GIVEN, SCALE, TO>, sizeof(FwdSmem<TX, TG>), p,
+                         ch, vec, &cs, s);
   }
 };
 struct StepRun {
@@ -227,37 +200,25 @@ struct StepRun {
   cudaStream_t s;
   template <typename TX, typename TG, bool GIVEN, int SCALE, bool WIDE>
   cudaError_t run() const {
-    const long long blocks = (long long)p.B * ((p.D + 127) / 128);
+    const long long blocks = (long long)p.B * ((p.D + 255) / 256);
     linrec_step_kernel<TX, TG, GIVEN, SCALE, typename Wide<TX, WIDE>::type>
         <<<(unsigned)blocks, 128, 0, s>>>(p, state);
     return cudaGetLastError();
   }
 };
 
-bool any_neighbours(const LinrecArgs& a) {
-  if (a.cu == nullptr) return a.T > kLinrecChunk;
-  for (int i = 0; i < a.B; ++i)
-    if (a.cu[i + 1] - a.cu[i] > kLinrecChunk) return true;
-  return false;
-}
-
 }  // namespace
 
-// Workspace: the sequence table; the ticket and a flag a tile; the tiles' aggregates; the
-// chunks' carries.
+// Workspace: the table of a packed batch.
 size_t linrec_workspace_bytes(const long long* cu, int B, int T, int D) {
-  return chain_bytes(cu, B, T, D);
+  return cu ? seq_table_bytes(B) : 0;
 }
 
-cudaError_t make_chain(const LinrecArgs& a, void* workspace, float* carry, bool table,
-                       cudaStream_t s, Chain* ch) {
-  char* ws = static_cast<char*>(workspace);
-  const long long chunks = linrec_chunks(a.cu, a.B, a.T);
-  ch->B = a.B; ch->T = a.T; ch->D = a.D;
+cudaError_t make_chains(const LinrecArgs& a, void* workspace, bool table, cudaStream_t s,
+                        Chains* ch) {
   ch->nblk = (a.D + kTileC - 1) / kTileC;
-  ch->per_row = (int)(((long long)a.T + kTileT - 1) / kTileT);
-  ch->tiles = (int)(chunks * ch->nblk);
   if (a.cu) {
+    char* ws = static_cast<char*>(workspace);
     ch->tab.cu = reinterpret_cast<const long long*>(ws);
     ch->tab.chunk0 =
         reinterpret_cast<const int*>(ws + align256((size_t)(a.B + 1) * sizeof(long long)));
@@ -265,42 +226,24 @@ cudaError_t make_chain(const LinrecArgs& a, void* workspace, float* carry, bool 
       cudaError_t e = fill_seq_table(a.cu, a.B, ch->tab, s);
       if (e != cudaSuccess) return e;
     }
-    ws += seq_table_bytes(a.B);
   }
-  const size_t flag_bytes = flags_bytes(ch->tiles);
-  ch->ticket = any_neighbours(a) ? reinterpret_cast<int*>(ws) : nullptr;
-  ch->flags = reinterpret_cast<int*>(ws) + 64;
-  ch->agg = reinterpret_cast<float4*>(ws + flag_bytes);
-  ch->carry = carry ? carry
-                    : reinterpret_cast<float*>(ws + flag_bytes + (size_t)ch->tiles * 32 * sizeof(float4));
   ch->status = status_word();
   if (ch->status == nullptr) return cudaErrorUnknown;
   const WaitFault wf = wait_fault();
-  ch->spin = wf.spin < kLinrecSpin ? wf.spin : kLinrecSpin;
+  ch->spin = wf.spin;
   ch->fault = wf.site == kFaultLinrec;
-  return ch->ticket ? cudaMemsetAsync(ws, 0, flag_bytes, s) : cudaSuccess;
+  return cudaSuccess;
 }
 
-cudaError_t copy_empty(const LinrecArgs& a, const Chain& ch, const float* src, float* dst,
-                       cudaStream_t s) {
-  if (a.cu == nullptr || dst == nullptr || src == dst) return cudaSuccess;
-  bool any = false;
-  for (int i = 0; i < a.B; ++i) any |= a.cu[i + 1] == a.cu[i];
-  if (!any) return cudaSuccess;
-  copy_empty_kernel<<<a.B, 128, 0, s>>>(ch.tab.cu, a.D, src, dst);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_linrec_scan(const LinrecArgs& a, const Chain& ch, int wide_flag,
+cudaError_t launch_linrec_scan(const LinrecArgs& a, const Chains& ch, int wide_flag,
                                cudaStream_t s) {
   return by_type(a, wide_flag, FwdRun{a, ch, s});
 }
 
 cudaError_t launch_linrec_fwd(const LinrecArgs& a, void* workspace, cudaStream_t s) {
-  Chain ch{};
-  cudaError_t e = make_chain(a, workspace, a.states_out, true, s, &ch);
-  if (e == cudaSuccess) e = launch_linrec_scan(a, ch, GDN_OUT_F32, s);
-  return e != cudaSuccess ? e : copy_empty(a, ch, a.h0, a.ht, s);
+  Chains ch{};
+  cudaError_t e = make_chains(a, workspace, true, s, &ch);
+  return e != cudaSuccess ? e : launch_linrec_scan(a, ch, GDN_OUT_F32, s);
 }
 
 cudaError_t launch_linrec_step(const LinrecArgs& a, float* state, cudaStream_t s) {

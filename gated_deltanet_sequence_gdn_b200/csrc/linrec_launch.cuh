@@ -1,37 +1,22 @@
 // linrec_launch.cuh -- host side shared by the scan and the backward of the gated linear
-// recurrence: workspace layout, choice of the kernel by type, the persistent launch.
+// recurrence: workspace layout, choice of the kernel by type, the launch.
 #pragma once
 
-#include "linrec_chain.cuh"
+#include "linrec_tile.cuh"
 
 namespace gdn {
-
-constexpr unsigned kLinrecSpin = 1u << 21;  // polls of a neighbour's flag before giving up (> 1 s)
 
 inline size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 inline size_t seq_table_bytes(int B) {
   return align256((size_t)(B + 1) * sizeof(long long)) + align256((size_t)(B + 1) * sizeof(int));
 }
-inline size_t flags_bytes(long long tiles) { return align256(256 + (size_t)tiles * sizeof(int)); }
-inline size_t carry_bytes(long long chunks, int D) {
-  return align256((size_t)chunks * D * sizeof(float));
-}
-inline size_t chain_bytes(const long long* cu, int B, int T, int D) {
-  const long long chunks = linrec_chunks(cu, B, T), tiles = chunks * ((D + kTileC - 1) / kTileC);
-  return (cu ? seq_table_bytes(B) : 0) + flags_bytes(tiles) +
-         (size_t)tiles * 32 * sizeof(float4) + carry_bytes(chunks, D);
-}
 
-// Lays the chain's arrays out in the workspace, writes the sequence table (`table`) and
-// clears the flags.  carry: where the tiles' carries go (NULL: into the workspace).
-cudaError_t make_chain(const LinrecArgs& a, void* workspace, float* carry, bool table,
-                       cudaStream_t s, Chain* ch);
-// The forward scan on a chain; wide_flag: the call's flag for float32 outputs.
-cudaError_t launch_linrec_scan(const LinrecArgs& a, const Chain& ch, int wide_flag,
+// Fills in what every launch of a call shares; `table`: writes the table of a packed batch.
+cudaError_t make_chains(const LinrecArgs& a, void* workspace, bool table, cudaStream_t s,
+                        Chains* ch);
+// The forward scan; wide_flag: the call's flag for float32 outputs.
+cudaError_t launch_linrec_scan(const LinrecArgs& a, const Chains& ch, int wide_flag,
                                cudaStream_t s);
-// Rows of dst that belong to empty sequences: src's (zeros where NULL).
-cudaError_t copy_empty(const LinrecArgs& a, const Chain& ch, const float* src, float* dst,
-                       cudaStream_t s);
 
 // Rows that start on 16 bytes; rows whose element pairs are aligned.
 inline int rows16(const void* p, long long ld, int es) {
@@ -41,21 +26,58 @@ inline int pairs(const void* p, long long ld, int es) {
   return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(ld * es)) & (2 * es - 1)) == 0;
 }
 
-// One block a slot of the machine (or a tile, where those are fewer).
+// The most blocks that one chain can use.
+inline int most_blocks(const LinrecArgs& p) {
+  long long longest = p.T;
+  if (p.cu) {
+    longest = 0;
+    for (int i = 0; i < p.B; ++i)
+      longest = p.cu[i + 1] - p.cu[i] > longest ? p.cu[i + 1] - p.cu[i] : longest;
+  }
+  int cs = 1;
+  while (cs < kMaxCluster && (long long)cs * kTileT < longest) cs *= 2;
+  return cs;
+}
+// Blocks of a cluster: as many as still leave every block of the launch a place on the
+// machine (`slots` blocks run at once).
+inline int cluster_size(const LinrecArgs& p, long long chains, int slots) {
+  const int most = most_blocks(p);
+  int cs = 1;
+  while (cs < most && chains * cs * 2 <= slots) cs *= 2;
+  return cs;
+}
+
 template <typename K, typename... More>
-cudaError_t launch_chain(K kernel, size_t smem, const LinrecArgs& p, const Chain& ch, int vec,
-                         cudaStream_t s, More... more) {
+cudaError_t launch_chains(K kernel, size_t smem, const LinrecArgs& p, const Chains& chains,
+                          int vec, int* cluster, cudaStream_t s, More... more) {
   int dev = 0, sms = 0, per = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const size_t most = smem + 2 * kMaxCluster * sizeof(FoldRow);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess)
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kLinrecThreads, smem);
   if (e != cudaSuccess) return e;
-  const long long most = (long long)sms * (per > 0 ? per : 1);
-  kernel<<<(unsigned)(ch.tiles < most ? ch.tiles : most), kLinrecThreads, smem, s>>>(p, ch, vec, more...);
-  return cudaGetLastError();
+  Chains ch = chains;
+  const long long n = (long long)p.B * ch.nblk;
+  ch.cs = cluster_size(p, n, sms * (per > 0 ? per : 1));
+  *cluster = ch.cs;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)ch.cs;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(n * ch.cs));
+  cfg.blockDim = dim3(kLinrecThreads);
+  cfg.dynamicSmemBytes = smem + (ch.cs > 1 ? 2 * ch.cs * sizeof(FoldRow) : 0);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = ch.cs > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, p, ch, vec, more...);
 }
 
 // Calls f.template run<TX, TG, GIVEN, SCALE, WIDE>() for the call's types: x in TX, the gates

@@ -2,10 +2,11 @@
 // backward and its one-token step:
 //   z = a + dt_bias, g = -e^{A_log} softplus(z), alpha = e^g, beta = sigmoid(b),
 //   f = 1, 1 - alpha or sqrt(1 - alpha^2) (the input scale), u = f beta x.
-// float32 throughout.  Every exponential is one SFU ex2 of a rounded product and every
-// quotient one SFU reciprocal (about 1e-7 relative each); 1 - alpha and softplus are
-// evaluated so that they keep their relative accuracy where they are small (slow
-// channels, whose alpha is next to 1).
+// float32 throughout, two channels at a time (packed f32x2 arithmetic halves the
+// instructions, which is what bounds these kernels).  Every exponential is one SFU ex2 of a
+// rounded product and every quotient one SFU reciprocal (about 1e-7 relative each);
+// 1 - alpha and softplus keep their relative accuracy where they are small (slow channels,
+// whose alpha is next to 1).  The decay is carried as its base-2 exponent e = g log2(e).
 #pragma once
 
 #include "common.cuh"
@@ -13,6 +14,7 @@
 namespace gdn {
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
 // Input scale of the recurrence (GDN_LINREC_TIED, GDN_LINREC_UNIT).
 enum LinrecScale { kScaleNone = 0, kScaleTied = 1, kScaleUnit = 2 };
@@ -33,40 +35,115 @@ __device__ __forceinline__ float sqrt_f(float x) {
   return y;
 }
 
-// log(1 + y) for y in [0, 1]: 2 atanh(t), t = y / (2 + y) <= 1/3, by its odd series;
-// the first term left out is t^14 / 15 < 1.4e-8 relative.
-__device__ __forceinline__ float log1p_unit(float y, float inv_2py) {
-  const float t = y * inv_2py, w = t * t;
-  float p = fmaf(w, 1.f / 13.f, 1.f / 11.f);
-  p = fmaf(w, p, 1.f / 9.f);
-  p = fmaf(w, p, 1.f / 7.f);
-  p = fmaf(w, p, 1.f / 5.f);
-  p = fmaf(w, p, 1.f / 3.f);
-  p = fmaf(w, p, 1.f);
-  return 2.f * t * p;
+// Two floats in one 64-bit register pair.
+union F2 {
+  unsigned long long u;
+  float2 f;
+};
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  F2 x, y, z, r;
+  x.f = a; y.f = b; z.f = c;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.u) : "l"(x.u), "l"(y.u), "l"(z.u));
+  return r.f;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  F2 x, y, r;
+  x.f = a; y.f = b;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(x.u), "l"(y.u));
+  return r.f;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  F2 x, y, r;
+  x.f = a; y.f = b;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(x.u), "l"(y.u));
+  return r.f;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 ex2_2(float2 x) { return make_float2(ex2_f(x.x), ex2_f(x.y)); }
+__device__ __forceinline__ float2 rcp_2(float2 x) { return make_float2(rcp_f(x.x), rcp_f(x.y)); }
+
+// log(1 + y) / y for y in [0, 1]: the polynomial of degree 8 with the least relative error
+// (Remez exchange on log1p(y) / y; 3.0e-8, 1.7e-7 with float32 rounding).
+__device__ __forceinline__ float2 log1p_over(float2 y) {
+  float2 p = both(5.232694263e-03f);
+  p = fma2(p, y, both(-2.950523877e-02f));
+  p = fma2(p, y, both(7.822595187e-02f));
+  p = fma2(p, y, both(-1.366324579e-01f));
+  p = fma2(p, y, both(1.910600676e-01f));
+  p = fma2(p, y, both(-2.484298221e-01f));
+  p = fma2(p, y, both(3.331909681e-01f));
+  p = fma2(p, y, both(-4.999949314e-01f));
+  return fma2(p, y, both(9.999999699e-01f));
 }
 
-// 1 - e^v for v <= 0: the exponential's series where it would cancel (v > -0.35: the
-// first term left out is v^7 / 8! < 2e-8 relative), the difference elsewhere.
-__device__ __forceinline__ float one_minus_exp(float v) {
-  float p = fmaf(v, 1.f / 5040.f, 1.f / 720.f);
-  p = fmaf(v, p, 1.f / 120.f);
-  p = fmaf(v, p, 1.f / 24.f);
-  p = fmaf(v, p, 1.f / 6.f);
-  p = fmaf(v, p, 0.5f);
-  p = fmaf(v, p, 1.f);
-  return v > -0.35f ? -v * p : 1.f - ex2_f(v * kLog2e);
+// 1 - 2^e for e <= 0: the exponential's series in v = e ln 2 where the difference would
+// cancel (v > -0.35: the first term left out is v^7 / 8! < 2e-8 relative), 1 - pow elsewhere
+// (pow = 2^e).
+__device__ __forceinline__ float2 one_minus_ex2(float2 e, float2 pow) {
+  const float2 v = mul2(e, both(kLn2));
+  float2 p = fma2(v, both(1.f / 5040.f), both(1.f / 720.f));
+  p = fma2(v, p, both(1.f / 120.f));
+  p = fma2(v, p, both(1.f / 24.f));
+  p = fma2(v, p, both(1.f / 6.f));
+  p = fma2(v, p, both(0.5f));
+  p = fma2(v, p, both(1.f));
+  p = mul2(v, p);
+  return make_float2(e.x > -0.5f ? -p.x : 1.f - pow.x, e.y > -0.5f ? -p.y : 1.f - pow.y);
 }
 
-// The input scale f and, for the backward, df/dg = f' (alpha' = alpha with respect to g).
-// sqrt(1 - alpha^2) has an infinite slope at g = 0; what reaches a is f' dg/da, which goes
-// to 0 there with softplus, so f' is taken as 0 where f underflows.
+// Per-channel constants of the gates.
+struct GateConst {
+  float2 rate;  // -e^{A_log} log2(e): e = rate softplus(z)
+  float2 bias;  // dt_bias
+};
+__device__ __forceinline__ GateConst gate_const(const float* A_log, const float* dt_bias, int c,
+                                                int D) {
+  GateConst k{both(0.f), both(0.f)};
+  if (c < D) {
+    k.rate.x = -expf(A_log[c]) * kLog2e;
+    k.bias.x = dt_bias[c];
+  }
+  if (c + 1 < D) {
+    k.rate.y = -expf(A_log[c + 1]) * kLog2e;
+    k.bias.y = dt_bias[c + 1];
+  }
+  return k;
+}
+
+// The base-2 exponent of alpha; GIVEN: a is g itself.  softplus(z) = max(z, 0) + log(1 + y)
+// with y = e^{-|z|}.
+template <bool GIVEN>
+__device__ __forceinline__ float2 decay_exponent(float2 a, const GateConst& k) {
+  if (GIVEN) return mul2(a, both(kLog2e));
+  const float2 z = add2(a, k.bias);
+  const float2 y = make_float2(ex2_f(-fabsf(z.x) * kLog2e), ex2_f(-fabsf(z.y) * kLog2e));
+  const float2 m = make_float2(fmaxf(z.x, 0.f), fmaxf(z.y, 0.f));  // a NaN goes through y
+  return mul2(k.rate, fma2(y, log1p_over(y), m));
+}
+// The same, and slope = -e^{A_log} sigmoid(z), the derivative of g with respect to a.
+__device__ __forceinline__ float2 decay_exponent_slope(float2 a, const GateConst& k,
+                                                       float2* slope) {
+  const float2 z = add2(a, k.bias);
+  const float2 y = make_float2(ex2_f(-fabsf(z.x) * kLog2e), ex2_f(-fabsf(z.y) * kLog2e));
+  const float2 r = rcp_2(add2(y, both(1.f)));
+  const float2 sg = make_float2(z.x >= 0.f ? r.x : r.x * y.x, z.y >= 0.f ? r.y : r.y * y.y);
+  *slope = mul2(mul2(k.rate, both(kLn2)), sg);
+  const float2 m = make_float2(fmaxf(z.x, 0.f), fmaxf(z.y, 0.f));
+  return mul2(k.rate, fma2(y, log1p_over(y), m));
+}
+
+// The input scale f from alpha = 2^e.
 template <int SCALE>
-__device__ __forceinline__ float input_scale(float g) {
-  if (SCALE == kScaleTied) return one_minus_exp(g);
-  if (SCALE == kScaleUnit) return sqrt_f(one_minus_exp(2.f * g));
-  return 1.f;
+__device__ __forceinline__ float2 input_scale(float2 e, float2 alpha) {
+  if (SCALE == kScaleTied) return one_minus_ex2(e, alpha);
+  if (SCALE == kScaleUnit) {
+    const float2 q = one_minus_ex2(add2(e, e), mul2(alpha, alpha));
+    return make_float2(sqrt_f(q.x), sqrt_f(q.y));
+  }
+  return both(1.f);
 }
+// df/dg.  sqrt(1 - alpha^2) has an infinite slope at g = 0; what reaches a is f' dg/da, which
+// goes to 0 there with softplus, so f' is taken as 0 where f underflows.
 template <int SCALE>
 __device__ __forceinline__ float input_scale_slope(float alpha, float f) {
   if (SCALE == kScaleTied) return -alpha;
@@ -74,32 +151,17 @@ __device__ __forceinline__ float input_scale_slope(float alpha, float f) {
   return 0.f;
 }
 
-// Per-channel constants of the gates.
-struct GateConst {
-  float neg_A;  // -e^{A_log}
-  float bias;   // dt_bias
-};
-__device__ __forceinline__ GateConst gate_const(const float* A_log, const float* dt_bias, int c) {
-  return GateConst{-expf(A_log[c]), dt_bias[c]};
-}
-
-// The log-decay g of one element; `given`: a is g itself.
+// beta; GIVEN: b is beta itself.
 template <bool GIVEN>
-__device__ __forceinline__ float log_decay(float a, const GateConst& k) {
-  if (GIVEN) return a;
-  const float z = a + k.bias;
-  const float y = ex2_f(-fabsf(z) * kLog2e);
-  return k.neg_A * (fmaxf(z, 0.f) + log1p_unit(y, rcp_f(2.f + y)));
+__device__ __forceinline__ float2 write_gate(float2 b) {
+  if (GIVEN) return b;
+  return rcp_2(add2(ex2_2(mul2(b, both(-kLog2e))), both(1.f)));
 }
-// sigmoid by the exponential that does not overflow.
-__device__ __forceinline__ float sigmoid_sfu(float b) {
-  const float e = ex2_f(-fabsf(b) * kLog2e);
-  const float r = rcp_f(1.f + e);
-  return b >= 0.f ? r : e * r;
-}
-template <bool GIVEN>
-__device__ __forceinline__ float write_gate(float b) {
-  return GIVEN ? b : sigmoid_sfu(b);
+// 1 - beta = beta e^{-b}, without the cancellation (the exponent is kept below 2^126, where
+// beta has underflowed).
+__device__ __forceinline__ float2 write_gate_rest(float2 b, float2 beta) {
+  const float2 e = mul2(b, both(-kLog2e));
+  return mul2(beta, make_float2(ex2_f(fminf(e.x, 126.f)), ex2_f(fminf(e.y, 126.f))));
 }
 
 }  // namespace gdn

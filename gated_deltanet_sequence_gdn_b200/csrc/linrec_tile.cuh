@@ -1,0 +1,234 @@
+// linrec_tile.cuh -- what the scan of the gated linear recurrence and the reverse scan of
+// its backward share: tiles of 64 tokens x 64 channels, their rows copied to shared memory
+// ahead of use, and the carry from tile to tile.
+//
+// A chain is one sequence's 64 channels; its tiles are taken in turn by the blocks of one
+// thread-block cluster (1 to 16 blocks: as many as it takes to fill the machine).  A tile is
+// 8 warps x 8 tokens; a lane holds 2 adjacent channels.  Each thread folds its 8 tokens into
+// (A, H): carry_out = A carry_in + H; the folds of the 8 warps meet in shared memory, so that
+// within a tile the recurrence is 8 + 8 steps instead of 64.  The blocks of a cluster send
+// their tiles' (A, H) to one another through distributed shared memory, counted on the
+// receiver's mbarrier, and each runs the same carry through the tiles of the round.  The
+// carry is folded tile by tile in order whatever the cluster's size, so the result does not
+// depend on it.
+#pragma once
+
+#include "common.cuh"
+#include "launch.h"
+#include "linrec.cuh"
+#include "linrec_math.cuh"
+#include "tc_ptx.cuh"
+
+namespace gdn {
+
+constexpr int kTileT = kLinrecChunk;  // tokens of a tile
+constexpr int kTileC = 64;            // channels of a tile
+constexpr int kWarps = 8;             // of a block, 8 tokens each
+constexpr int kPer = kTileT / kWarps;
+constexpr int kLinrecThreads = kWarps * 32;
+constexpr int kMaxCluster = 16;
+
+// Packed batches: each sequence's first token and first chunk, entry B the totals.
+struct SeqTab {
+  const long long* cu;  // NULL: dense rows
+  const int* chunk0;
+};
+
+// One launch: the chains by cluster, row by row of the batch.
+struct Chains {
+  SeqTab tab;
+  int nblk;  // chains of a sequence
+  int cs;    // blocks of a cluster
+  int* status;
+  unsigned spin;  // polls before a wait gives up
+  bool fault;     // test hook: the first block of a cluster keeps its folds to itself
+};
+
+// One chain, as a block of its cluster sees it.
+struct Chain {
+  long long tok;   // the sequence's first token (row of the tensors)
+  long long len;   // its tokens
+  long long chunk0;
+  int row, c0;     // sequence, first channel
+  int chunks, rank;
+};
+__device__ __forceinline__ Chain chain_of(const LinrecArgs& p, const Chains& ch) {
+  Chain k;
+  const int id = blockIdx.x / ch.cs;
+  k.rank = blockIdx.x % ch.cs;
+  k.row = id / ch.nblk;
+  k.c0 = (id - k.row * ch.nblk) * kTileC;
+  if (ch.tab.cu == nullptr) {
+    k.tok = (long long)k.row * p.T;
+    k.len = p.T;
+    k.chunk0 = (long long)k.row * ((p.T + (long long)kTileT - 1) / kTileT);
+  } else {
+    k.tok = ch.tab.cu[k.row];
+    k.len = ch.tab.cu[k.row + 1] - k.tok;
+    k.chunk0 = ch.tab.chunk0[k.row];
+  }
+  k.chunks = (int)((k.len + kTileT - 1) / kTileT);
+  return k;
+}
+
+// Shared memory of the carry: each warp's fold, the carry into the tile, and behind the
+// kernel's own shared memory the cluster's folds, [2 rounds][cs][32].
+struct CarrySmem {
+  float4 fold[kWarps][32];  // (A, A', H, H') of a lane's two channels
+  float2 in[32];
+  uint64_t full[2];  // the round's folds have arrived
+};
+using FoldRow = float4[32];
+
+__device__ __forceinline__ float2 first2(float4 v) { return make_float2(v.x, v.y); }
+__device__ __forceinline__ float2 last2(float4 v) { return make_float2(v.z, v.w); }
+__device__ __forceinline__ float4 join4(float2 a, float2 b) {
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+
+__device__ __forceinline__ void st_async_peer(uint32_t addr, float4 v, uint32_t bar_addr) {
+  asm volatile(
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+          addr),
+      "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar_addr)
+      : "memory");
+}
+
+// One round of the carry, by one warp: own is this block's tile's (A, H).  Returns what
+// enters the tile and moves `carry` behind the round's last tile.  `lost`: a wait has
+// expired, later ones are not tried.
+__device__ __forceinline__ float2 carry_round(const Chains& ch, int rank, int round, float4 own,
+                                              CarrySmem& sm, FoldRow* folds, float2* carry,
+                                              bool* lost) {
+  if (ch.cs == 1) {
+    const float2 in = *carry;
+    *carry = fma2(first2(own), in, last2(own));
+    return in;
+  }
+  const int lane = threadIdx.x & 31, buf = round & 1;
+  FoldRow* row = folds + buf * ch.cs;
+  if (lane == 0)
+    tc::mbar_arrive_expect_tx(&sm.full[buf], (uint32_t)(ch.cs * 32 * sizeof(float4)));
+  __syncwarp();
+  if (!*lost && !(ch.fault && rank == 0))  // nothing is under way to a peer that has given up
+    for (int r = 0; r < ch.cs; ++r)
+      st_async_peer(tc::map_peer(&row[rank][lane], r), own, tc::map_peer(&sm.full[buf], r));
+  if (!*lost) {
+    const bool ok = tc::mbar_wait(&sm.full[buf], (round >> 1) & 1, nullptr, 0, ch.spin);
+    *lost = !__all_sync(0xffffffffu, ok);
+    if (*lost && lane == 0) report_timeout(ch.status, 0x4c52);
+  }
+  float2 in = *carry, v = *carry;
+  for (int r = 0; r < ch.cs; ++r) {
+    if (r == rank) in = v;
+    const float4 f = row[r][lane];
+    v = fma2(first2(f), v, last2(f));
+  }
+  *carry = v;
+  return in;
+}
+
+__device__ __forceinline__ void carry_begin(const Chains& ch, CarrySmem& sm) {
+  if (threadIdx.x == 0) {
+    tc::mbar_init(&sm.full[0], 1);
+    tc::mbar_init(&sm.full[1], 1);
+    tc::fence_mbar_init();
+  }
+  __syncwarp();
+  if (ch.cs > 1) tc::cluster_sync();  // the barriers are there before a peer counts on them
+}
+// No block leaves while a peer may still send to it.
+__device__ __forceinline__ void carry_end(const Chains& ch) {
+  __syncwarp();
+  if (ch.cs > 1) tc::cluster_sync();
+}
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(dst)),
+               "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async4(void* dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(tc::smem_u32(dst)), "l"(src),
+               "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// `n` tokens of one tensor from row `tok` on to shared memory [64][64], zeros behind them and
+// behind the last channel; `vec`: rows start on 16 bytes and move in 16-byte pieces.
+template <typename T>
+__device__ __forceinline__ void load_tile(T* dst, const void* base, long long ld, long long tok,
+                                          int n, int c0, int D, bool vec) {
+  const T* src = static_cast<const T*>(base) + tok * ld + c0;
+  const int cols = D - c0 < kTileC ? D - c0 : kTileC;
+  if (vec) {
+    constexpr int E = 16 / sizeof(T), P = kTileC / E;  // elements of a piece, pieces of a row
+    constexpr int kRows = kLinrecThreads / P;          // rows of a step
+    const int r0 = threadIdx.x / P, c = (threadIdx.x % P) * E;
+    const int left = cols - c, bytes = (left < 0 ? 0 : left < E ? left : E) * (int)sizeof(T);
+    src += r0 * ld + c;
+    dst += r0 * kTileC + c;
+#pragma unroll
+    for (int i = 0; i < kTileT / kRows; ++i) {
+      const int in = r0 + i * kRows < n ? bytes : 0;
+      cp_async16(dst + i * kRows * kTileC, in ? static_cast<const void*>(src) : base, in);
+      src += kRows * ld;
+    }
+  } else {
+#pragma unroll 4
+    for (int i = 0; i < kTileT * kTileC / kLinrecThreads; ++i) {
+      const int k = threadIdx.x + i * kLinrecThreads, r = k / kTileC, c = k % kTileC;
+      const bool in = r < n && c < cols;
+      if (sizeof(T) == 4)
+        cp_async4(dst + r * kTileC + c, in ? static_cast<const void*>(src + r * ld + c) : base,
+                  in ? 4 : 0);
+      else
+        dst[r * kTileC + c] = in ? src[r * ld + c] : from_f32<T>(0.f);
+    }
+  }
+}
+
+// A lane's two channels.
+__device__ __forceinline__ float2 get2(const float* p) { return *reinterpret_cast<const float2*>(p); }
+__device__ __forceinline__ float2 get2(const __nv_bfloat16* p) {
+  const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
+  return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+// `cols` of them are inside; `pair`: the two may be stored at once.
+__device__ __forceinline__ void put2(float* p, float2 v, int cols, bool pair) {
+  if (pair && cols > 1) {
+    *reinterpret_cast<float2*>(p) = v;
+  } else {
+    if (cols > 0) p[0] = v.x;
+    if (cols > 1) p[1] = v.y;
+  }
+}
+__device__ __forceinline__ void put2(__nv_bfloat16* p, float2 v, int cols, bool pair) {
+  if (pair && cols > 1) {
+    *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(v.x, v.y);
+  } else {
+    if (cols > 0) p[0] = __float2bfloat16_rn(v.x);
+    if (cols > 1) p[1] = __float2bfloat16_rn(v.y);
+  }
+}
+// Two floats of a [.., D] array at channel c (0 outside, or where the array is NULL).
+__device__ __forceinline__ float2 read2(const float* base, long long row, int c, int D) {
+  if (base == nullptr) return both(0.f);
+  base += row * D + c;
+  return make_float2(c < D ? base[0] : 0.f, c + 1 < D ? base[1] : 0.f);
+}
+__device__ __forceinline__ void write2(float* base, long long row, int c, int D, float2 v) {
+  if (base == nullptr) return;
+  base += row * D + c;
+  if (c < D) base[0] = v.x;
+  if (c + 1 < D) base[1] = v.y;
+}
+
+}  // namespace gdn

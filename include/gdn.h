@@ -502,9 +502,10 @@ size_t gdn2_chunk_workspace_bytes(int B, int T, int H, int dk, int dv, int dtype
  *              Calls that may run at the same time need a workspace each.
  *   Every pointer needs its element alignment only (rows that are 16-byte aligned move
  *   in 16-byte pieces).  States and sums are float32, outputs rounded once; the result
- *   does not depend on how the work was scheduled.  T = 0 and empty sequences copy h0
- *   to ht (or zeros).  The kernels wait for one another's chunk states, with a limit:
- *   an expired wait is reported by gdn_check_status.
+ *   does not depend on how the work was split.  T = 0 and empty sequences copy h0 to ht
+ *   (or zeros).  Long sequences of few channels are taken by clusters of thread blocks
+ *   that wait for one another, with a limit: an expired wait is reported by
+ *   gdn_check_status.
  */
 int gdn_linrec_fwd(const void* x, const void* a, const void* b, const float* A_log,
                    const float* dt_bias, const float* h0, const long long* cu_seqlens, int B,
@@ -512,7 +513,8 @@ int gdn_linrec_fwd(const void* x, const void* a, const void* b, const float* A_l
                    int flags, void* h, long long ldh, float* ht, float* states,
                    void* workspace, size_t ws_bytes, gdn_stream_t stream);
 
-/* Device workspace bytes gdn_linrec_fwd needs (0 for invalid sizes). */
+/* Device workspace bytes gdn_linrec_fwd needs: the table of a packed batch, 0 without
+ * cu_seqlens and for invalid sizes. */
 size_t gdn_linrec_workspace_bytes(const long long* cu_seqlens, int B, int T, int D);
 
 /*
@@ -637,8 +639,8 @@ int gdn_check_status(gdn_stream_t stream);
  *   site 1: the state scan issues no first products, so its epilogue's wait for
  *           them expires;
  *   site 2: the WY prep withholds its K / Q tile loads;
- *   site 3: the linear recurrence's first chunks do not publish their states, so the
- *           waits of the chunks after them expire.
+ *   site 3: the linear recurrence: the first block of a cluster keeps its chunks'
+ *           results to itself, so the waits of the others expire.
  *   spin_limit: polls before a wait gives up, for every bounded wait of those
  *   kernels (0 = the default, 2^24).  The setting is process-wide and stays
  *   until changed; the outputs of a faulted call are not valid.
