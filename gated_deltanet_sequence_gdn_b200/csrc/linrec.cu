@@ -63,16 +63,26 @@ linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec) {
     const long long left = k.len - (long long)tt * kTileT;
     const int n = left < kTileT ? (left < 0 ? 0 : (int)left) : kTileT;
     const FwdStage<TX, TG>& st = sm.stage[round & 1];
+    const int mine = warp * kPer * kTileC + 2 * lane;
     float2 al[kPer], u[kPer];
     float2 A = both(1.f), H = both(0.f);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int at = (warp * kPer + i) * kTileC + 2 * lane;
-      const float2 e = decay_exponent<GIVEN>(get2(st.a + at), gc);
-      al[i] = ex2_2(e);
-      u[i] = get2(st.x + at);
-      if (SCALE != kScaleNone) u[i] = mul2(u[i], input_scale<SCALE>(e, al[i]));
-      if (p.b) u[i] = mul2(u[i], write_gate<GIVEN>(get2(st.b + at)));
+    for (int i0 = 0; i0 < kPer; i0 += kGroup) {
+      float2 e[kGroup];
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i) e[i] = get2(st.a + mine + (i0 + i) * kTileC);
+      decay_exponents<GIVEN, kGroup>(e, gc);
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i) {
+        al[i0 + i] = ex2_2(e[i]);
+        u[i0 + i] = get2(st.x + mine + (i0 + i) * kTileC);
+        if (SCALE != kScaleNone)
+          u[i0 + i] = mul2(u[i0 + i], input_scale<SCALE>(e[i], al[i0 + i]));
+      }
+      if (p.b)
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i)
+          u[i0 + i] = mul2(u[i0 + i], write_gate<GIVEN>(get2(st.b + mine + (i0 + i) * kTileC)));
     }
     if (n < kTileT) {  // behind the sequence: the state passes through
 #pragma unroll
@@ -113,11 +123,20 @@ linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec) {
     if (p.h) {
       float2 h = fma2(A, sm.carry.in[lane], H);
       TO* out = static_cast<TO*>(p.h) + (k.tok + (long long)tt * kTileT + warp * kPer) * p.ldh + c;
+      if (n == kTileT && cols > 1 && (vec & 8)) {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        h = fma2(al[i], h, u[i]);
-        if (warp * kPer + i < n) put2(out, h, cols, vec & 8);
-        out += p.ldh;
+        for (int i = 0; i < kPer; ++i) {
+          h = fma2(al[i], h, u[i]);
+          put2(out, h);
+          out += p.ldh;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          h = fma2(al[i], h, u[i]);
+          if (warp * kPer + i < n) put2(out, h, cols);
+          out += p.ldh;
+        }
       }
     }
   }
@@ -139,13 +158,14 @@ __global__ void __launch_bounds__(128) linrec_step_kernel(LinrecArgs p, float* s
   if (cols <= 0) return;
   GateConst gc{both(0.f), both(0.f)};
   if (!GIVEN) gc = gate_const(p.A_log, p.dt_bias, c, p.D);
-  const float2 e = decay_exponent<GIVEN>(take2<TG>(p.a, r * p.lda + c, cols), gc);
+  float2 e = take2<TG>(p.a, r * p.lda + c, cols);
+  decay_exponents<GIVEN, 1>(&e, gc);
   const float2 al = ex2_2(e);
   float2 u = mul2(take2<TX>(p.x, r * p.ldx + c, cols), input_scale<SCALE>(e, al));
   if (p.b) u = mul2(u, write_gate<GIVEN>(take2<TG>(p.b, r * p.ldb + c, cols)));
   const float2 st = fma2(al, read2(state, r, c, p.D), u);
   write2(state, r, c, p.D, st);
-  put2(static_cast<TO*>(p.h) + r * p.ldh + c, st, cols, false);
+  put2(static_cast<TO*>(p.h) + r * p.ldh + c, st, cols);
 }
 
 constexpr int kPiece = 240;  // entries of a table piece passed by value (< 4 KB of arguments)

@@ -73,16 +73,22 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const float* states, float2*
     __syncthreads();  // the stage is complete, the other one free
     if (round + 1 < rounds) load(round + 1);
     const BwdStage<TX, TG, TD>& st = sm.stage[round & 1];
+    const int mine = first * kTileC + 2 * lane;
     float2 al[kPer], be[kPer], f[kPer];
     float2 hs = n > 0 ? read2(states, k.chunk0 + tt, c, p.D) : both(0.f);
     float2 A = both(1.f), H = both(0.f), R = both(0.f);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int at = (first + i) * kTileC + 2 * lane;
-      const float2 e = decay_exponent<GIVEN>(get2(st.a + at), gc);
-      al[i] = ex2_2(e);
-      f[i] = input_scale<SCALE>(e, al[i]);
-      be[i] = p.b ? write_gate<GIVEN>(get2(st.b + at)) : both(1.f);
+    for (int i0 = 0; i0 < kPer; i0 += kGroup) {
+      float2 e[kGroup];
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i) e[i] = get2(st.a + mine + (i0 + i) * kTileC);
+      decay_exponents<GIVEN, kGroup>(e, gc);
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i) {
+        al[i0 + i] = ex2_2(e[i]);
+        f[i0 + i] = input_scale<SCALE>(e[i], al[i0 + i]);
+        be[i0 + i] = p.b ? write_gate<GIVEN>(get2(st.b + mine + (i0 + i) * kTileC)) : both(1.f);
+      }
     }
     if (n < kTileT) {  // behind the sequence: both states pass through
 #pragma unroll
@@ -94,14 +100,14 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const float* states, float2*
     }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      float2 u = mul2(get2(st.x + (first + i) * kTileC + 2 * lane), be[i]);
+      float2 u = mul2(get2(st.x + mine + i * kTileC), be[i]);
       if (SCALE != kScaleNone) u = mul2(u, f[i]);
       H = fma2(al[i], H, u);
       A = mul2(A, al[i]);
     }
 #pragma unroll
     for (int i = kPer - 1; i >= 0; --i) {
-      if (first + i < n) R = add2(get2(st.dh + (first + i) * kTileC + 2 * lane), R);
+      if (first + i < n) R = add2(get2(st.dh + mine + i * kTileC), R);
       R = mul2(al[i], R);
     }
     sm.carry.fold[warp][lane] = join4(A, H);
@@ -128,46 +134,61 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const float* states, float2*
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       hp[i] = hs;
-      float2 u = mul2(get2(st.x + (first + i) * kTileC + 2 * lane), be[i]);
+      float2 u = mul2(get2(st.x + mine + i * kTileC), be[i]);
       if (SCALE != kScaleNone) u = mul2(u, f[i]);
       hs = fma2(al[i], hs, u);
     }
     float2 cc = fma2(A, sm.carry.in[lane], R);
     float2 tA = both(0.f), tb = both(0.f);
     const long long row = k.tok + (long long)tt * kTileT + first;
+    const bool whole = n == kTileT && cols > 1 && (vec & 0x70) == 0x70;
 #pragma unroll
-    for (int i = kPer - 1; i >= 0; --i) {
-      if (first + i >= n) continue;
-      const int at = (first + i) * kTileC + 2 * lane;
-      const float2 lam = add2(get2(st.dh + at), cc);
-      cc = mul2(al[i], lam);
-      const float2 lx = mul2(lam, get2(st.x + at));
-      float2 dg = mul2(cc, hp[i]);
-      if (SCALE != kScaleNone) {
-        const float2 q = make_float2(input_scale_slope<SCALE>(al[i].x, f[i].x),
-                                     input_scale_slope<SCALE>(al[i].y, f[i].y));
-        dg = fma2(mul2(lx, be[i]), q, dg);
-      }
-      float2 dx = mul2(lam, be[i]), db = lx;
-      if (SCALE != kScaleNone) {
-        dx = mul2(dx, f[i]);
-        db = mul2(db, f[i]);
-      }
-      put2(static_cast<TD*>(p.dx) + (row + i) * p.lddx + c, dx, cols, vec & 16);
-      if (p.b) {
-        if (!GIVEN) db = mul2(mul2(db, be[i]), write_gate_rest(get2(st.b + at), be[i]));
-        put2(static_cast<TDG*>(p.db) + (row + i) * p.lddb + c, db, cols, vec & 64);
-      }
-      float2 da = dg;
+    for (int i0 = kPer - kGroup; i0 >= 0; i0 -= kGroup) {
+      float2 e[kGroup], slope[kGroup];
       if (!GIVEN) {
-        float2 slope;
-        const float2 e = decay_exponent_slope(get2(st.a + at), gc, &slope);
-        da = mul2(dg, slope);
-        tb = add2(tb, da);
-        // dg log2(e) times e; e = -inf where alpha = 0
-        tA = add2(tA, make_float2(dg.x == 0.f ? 0.f : dg.x * e.x, dg.y == 0.f ? 0.f : dg.y * e.y));
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) e[i] = get2(st.a + mine + (i0 + i) * kTileC);
+        decay_exponents_slope<kGroup>(e, gc, slope);
       }
-      put2(static_cast<TDG*>(p.da) + (row + i) * p.ldda + c, da, cols, vec & 32);
+#pragma unroll
+      for (int j = kGroup - 1; j >= 0; --j) {
+        const int i = i0 + j, at = mine + i * kTileC;
+        if (first + i >= n) continue;
+        const float2 lam = add2(get2(st.dh + at), cc);
+        cc = mul2(al[i], lam);
+        const float2 lx = mul2(lam, get2(st.x + at));
+        float2 dg = mul2(cc, hp[i]);
+        if (SCALE != kScaleNone) {
+          const float2 q = make_float2(input_scale_slope<SCALE>(al[i].x, f[i].x),
+                                       input_scale_slope<SCALE>(al[i].y, f[i].y));
+          dg = fma2(mul2(lx, be[i]), q, dg);
+        }
+        float2 dx = mul2(lam, be[i]), db = lx, da = dg;
+        if (SCALE != kScaleNone) {
+          dx = mul2(dx, f[i]);
+          db = mul2(db, f[i]);
+        }
+        if (!GIVEN) {
+          if (p.b) db = mul2(mul2(db, be[i]), write_gate_rest(get2(st.b + at), be[i]));
+          da = mul2(dg, slope[j]);
+          tb = add2(tb, da);
+          // dg log2(e) times e; e = -inf where alpha = 0
+          tA = add2(tA, make_float2(dg.x == 0.f ? 0.f : dg.x * e[j].x,
+                                    dg.y == 0.f ? 0.f : dg.y * e[j].y));
+        }
+        TD* px = static_cast<TD*>(p.dx) + (row + i) * p.lddx + c;
+        TDG* pa = static_cast<TDG*>(p.da) + (row + i) * p.ldda + c;
+        TDG* pb = static_cast<TDG*>(p.db) + (row + i) * p.lddb + c;
+        if (whole) {
+          put2(px, dx);
+          put2(pa, da);
+          if (p.b) put2(pb, db);
+        } else {
+          put2(px, dx, cols);
+          put2(pa, da, cols);
+          if (p.b) put2(pb, db, cols);
+        }
+      }
     }
     if (!GIVEN) {  // a lane keeps its channels: their sums run through the rounds
       add_kept(&sA, &eA, tA);

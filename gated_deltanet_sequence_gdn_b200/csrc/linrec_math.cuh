@@ -63,17 +63,19 @@ __device__ __forceinline__ float2 ex2_2(float2 x) { return make_float2(ex2_f(x.x
 __device__ __forceinline__ float2 rcp_2(float2 x) { return make_float2(rcp_f(x.x), rcp_f(x.y)); }
 
 // log(1 + y) / y for y in [0, 1]: the polynomial of degree 8 with the least relative error
-// (Remez exchange on log1p(y) / y; 3.0e-8, 1.7e-7 with float32 rounding).
-__device__ __forceinline__ float2 log1p_over(float2 y) {
-  float2 p = both(5.232694263e-03f);
-  p = fma2(p, y, both(-2.950523877e-02f));
-  p = fma2(p, y, both(7.822595187e-02f));
-  p = fma2(p, y, both(-1.366324579e-01f));
-  p = fma2(p, y, both(1.910600676e-01f));
-  p = fma2(p, y, both(-2.484298221e-01f));
-  p = fma2(p, y, both(3.331909681e-01f));
-  p = fma2(p, y, both(-4.999949314e-01f));
-  return fma2(p, y, both(9.999999699e-01f));
+// (Remez exchange on log1p(y) / y; 3.0e-8, 1.7e-7 with float32 rounding).  N tokens at once:
+// a packed constant takes two moves into a register pair, so it is brought in once for all.
+template <int N>
+__device__ __forceinline__ void log1p_over(const float2* y, float2* p) {
+  const float k[9] = {5.232694263e-03f, -2.950523877e-02f, 7.822595187e-02f,
+                      -1.366324579e-01f, 1.910600676e-01f, -2.484298221e-01f,
+                      3.331909681e-01f, -4.999949314e-01f, 9.999999699e-01f};
+#pragma unroll
+  for (int i = 0; i < N; ++i) p[i] = fma2(y[i], both(k[0]), both(k[1]));
+#pragma unroll
+  for (int j = 2; j < 9; ++j)
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] = fma2(p[i], y[i], both(k[j]));
 }
 
 // 1 - 2^e for e <= 0: the exponential's series in v = e ln 2 where the difference would
@@ -110,26 +112,48 @@ __device__ __forceinline__ GateConst gate_const(const float* A_log, const float*
   return k;
 }
 
-// The base-2 exponent of alpha; GIVEN: a is g itself.  softplus(z) = max(z, 0) + log(1 + y)
-// with y = e^{-|z|}.
-template <bool GIVEN>
-__device__ __forceinline__ float2 decay_exponent(float2 a, const GateConst& k) {
-  if (GIVEN) return mul2(a, both(kLog2e));
-  const float2 z = add2(a, k.bias);
-  const float2 y = make_float2(ex2_f(-fabsf(z.x) * kLog2e), ex2_f(-fabsf(z.y) * kLog2e));
-  const float2 m = make_float2(fmaxf(z.x, 0.f), fmaxf(z.y, 0.f));  // a NaN goes through y
-  return mul2(k.rate, fma2(y, log1p_over(y), m));
+// e[i] in place of a[i], the base-2 exponents of alpha of N tokens; GIVEN: a is g itself.
+// softplus(z) = max(z, 0) + log(1 + y) with y = e^{-|z|}.
+template <bool GIVEN, int N>
+__device__ __forceinline__ void decay_exponents(float2* a, const GateConst& k) {
+  if (GIVEN) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) a[i] = mul2(a[i], both(kLog2e));
+    return;
+  }
+  float2 y[N], q[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    a[i] = add2(a[i], k.bias);
+    y[i] = make_float2(ex2_f(-fabsf(a[i].x) * kLog2e), ex2_f(-fabsf(a[i].y) * kLog2e));
+  }
+  log1p_over<N>(y, q);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {  // a NaN goes through y
+    const float2 m = make_float2(fmaxf(a[i].x, 0.f), fmaxf(a[i].y, 0.f));
+    a[i] = mul2(k.rate, fma2(y[i], q[i], m));
+  }
 }
 // The same, and slope = -e^{A_log} sigmoid(z), the derivative of g with respect to a.
-__device__ __forceinline__ float2 decay_exponent_slope(float2 a, const GateConst& k,
-                                                       float2* slope) {
-  const float2 z = add2(a, k.bias);
-  const float2 y = make_float2(ex2_f(-fabsf(z.x) * kLog2e), ex2_f(-fabsf(z.y) * kLog2e));
-  const float2 r = rcp_2(add2(y, both(1.f)));
-  const float2 sg = make_float2(z.x >= 0.f ? r.x : r.x * y.x, z.y >= 0.f ? r.y : r.y * y.y);
-  *slope = mul2(mul2(k.rate, both(kLn2)), sg);
-  const float2 m = make_float2(fmaxf(z.x, 0.f), fmaxf(z.y, 0.f));
-  return mul2(k.rate, fma2(y, log1p_over(y), m));
+template <int N>
+__device__ __forceinline__ void decay_exponents_slope(float2* a, const GateConst& k,
+                                                      float2* slope) {
+  float2 y[N], q[N];
+  const float2 rate = mul2(k.rate, both(kLn2));
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    a[i] = add2(a[i], k.bias);
+    y[i] = make_float2(ex2_f(-fabsf(a[i].x) * kLog2e), ex2_f(-fabsf(a[i].y) * kLog2e));
+    const float2 r = rcp_2(add2(y[i], both(1.f)));
+    slope[i] = mul2(rate, make_float2(a[i].x >= 0.f ? r.x : r.x * y[i].x,
+                                      a[i].y >= 0.f ? r.y : r.y * y[i].y));
+  }
+  log1p_over<N>(y, q);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float2 m = make_float2(fmaxf(a[i].x, 0.f), fmaxf(a[i].y, 0.f));
+    a[i] = mul2(k.rate, fma2(y[i], q[i], m));
+  }
 }
 
 // The input scale f from alpha = 2^e.

@@ -27,6 +27,7 @@ constexpr int kWarps = 8;             // of a block, 8 tokens each
 constexpr int kPer = kTileT / kWarps;
 constexpr int kLinrecThreads = kWarps * 32;
 constexpr int kMaxCluster = 16;
+constexpr int kGroup = 4;             // tokens whose gates are formed together
 
 // Packed batches: each sequence's first token and first chunk, entry B the totals.
 struct SeqTab {
@@ -175,6 +176,14 @@ __device__ __forceinline__ void load_tile(T* dst, const void* base, long long ld
     const int left = cols - c, bytes = (left < 0 ? 0 : left < E ? left : E) * (int)sizeof(T);
     src += r0 * ld + c;
     dst += r0 * kTileC + c;
+    if (n == kTileT && bytes == 16) {
+#pragma unroll
+      for (int i = 0; i < kTileT / kRows; ++i) {
+        cp_async16(dst + i * kRows * kTileC, src, 16);
+        src += kRows * ld;
+      }
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < kTileT / kRows; ++i) {
       const int in = r0 + i * kRows < n ? bytes : 0;
@@ -201,22 +210,15 @@ __device__ __forceinline__ float2 get2(const __nv_bfloat16* p) {
   const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
   return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
-// `cols` of them are inside; `pair`: the two may be stored at once.
-__device__ __forceinline__ void put2(float* p, float2 v, int cols, bool pair) {
-  if (pair && cols > 1) {
-    *reinterpret_cast<float2*>(p) = v;
-  } else {
-    if (cols > 0) p[0] = v.x;
-    if (cols > 1) p[1] = v.y;
-  }
+__device__ __forceinline__ void put2(float* p, float2 v) { *reinterpret_cast<float2*>(p) = v; }
+__device__ __forceinline__ void put2(__nv_bfloat16* p, float2 v) {
+  *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(v.x, v.y);
 }
-__device__ __forceinline__ void put2(__nv_bfloat16* p, float2 v, int cols, bool pair) {
-  if (pair && cols > 1) {
-    *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(v.x, v.y);
-  } else {
-    if (cols > 0) p[0] = __float2bfloat16_rn(v.x);
-    if (cols > 1) p[1] = __float2bfloat16_rn(v.y);
-  }
+// `cols` of them are inside, and a pair may not be aligned.
+template <typename T>
+__device__ __forceinline__ void put2(T* p, float2 v, int cols) {
+  if (cols > 0) p[0] = from_f32<T>(v.x);
+  if (cols > 1) p[1] = from_f32<T>(v.y);
 }
 // Two floats of a [.., D] array at channel c (0 outside, or where the array is NULL).
 __device__ __forceinline__ float2 read2(const float* base, long long row, int c, int D) {
