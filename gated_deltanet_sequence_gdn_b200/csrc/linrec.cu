@@ -17,9 +17,9 @@ namespace {
 
 template <typename TX, typename TG>
 struct FwdStage {
-  alignas(16) TX x[kTileT * kTileC];
-  alignas(16) TG a[kTileT * kTileC];
-  alignas(16) TG b[kTileT * kTileC];
+  alignas(128) TX x[kTileT * kTileC];
+  alignas(128) TG a[kTileT * kTileC];
+  alignas(128) TG b[kTileT * kTileC];
 };
 template <typename TX, typename TG>
 struct FwdSmem {
@@ -29,43 +29,61 @@ struct FwdSmem {
 
 template <typename TX, typename TG, bool GIVEN, int SCALE, typename TO>
 __global__ void __launch_bounds__(kLinrecThreads, sizeof(TX) + sizeof(TG) == 4 ? 4 : 2)
-linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec) {
-  extern __shared__ __align__(16) unsigned char smem_raw[];
+linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ LinrecMaps maps) {
+  extern __shared__ __align__(128) unsigned char smem_raw[];
   auto& sm = *reinterpret_cast<FwdSmem<TX, TG>*>(smem_raw);
   FoldRow* folds = reinterpret_cast<FoldRow*>(smem_raw + sizeof(FwdSmem<TX, TG>));
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const Chain k = chain_of(p, ch);
   const int c = k.c0 + 2 * lane, cols = p.D - c;
-  auto load = [&](int round) {
-    const int tt = round * ch.cs + k.rank;
-    if (tt < k.chunks) {
-      const long long left = k.len - (long long)tt * kTileT, tok = k.tok + (long long)tt * kTileT;
-      const int n = left < kTileT ? (int)left : kTileT;
-      FwdStage<TX, TG>& st = sm.stage[round & 1];
-      load_tile(st.x, p.x, p.ldx, tok, n, k.c0, p.D, vec & 1);
-      load_tile(st.a, p.a, p.lda, tok, n, k.c0, p.D, vec & 2);
-      if (p.b) load_tile(st.b, p.b, p.ldb, tok, n, k.c0, p.D, vec & 4);
-    }
-    cp_async_commit();
+  const int step = ch.cs * kTileT;
+  const int tokens = (int)k.len - k.rank * kTileT;  // from the block's first tile on
+  auto length = [&](int round) {
+    const int left = tokens - round * step;
+    return left < kTileT ? (left < 0 ? 0 : left) : kTileT;
   };
-  load(0);
+  auto load = [&](int round) {
+    const int n = length(round), t = (round * ch.cs + k.rank) * kTileT;
+    FwdStage<TX, TG>& st = sm.stage[round & 1];
+    if (ch.tma) {
+      if (n > 0 && threadIdx.x == 0) {
+        uint64_t* bar = &sm.carry.loaded[round & 1];
+        const int y = ch.tab.cu ? (int)k.tok + t : t, z = ch.tab.cu ? 0 : k.row;
+        tc::mbar_arrive_expect_tx(bar, sizeof(st.x) + sizeof(st.a) + (p.b ? sizeof(st.b) : 0));
+        tma_load_3d(st.x, &maps.x, bar, k.c0, y, z);
+        tma_load_3d(st.a, &maps.a, bar, k.c0, y, z);
+        if (p.b) tma_load_3d(st.b, &maps.b, bar, k.c0, y, z);
+      }
+    } else {
+      if (n > 0) {
+        load_elements(st.x, p.x, p.ldx, k.tok + t, n, k.c0, p.D);
+        load_elements(st.a, p.a, p.lda, k.tok + t, n, k.c0, p.D);
+        if (p.b) load_elements(st.b, p.b, p.ldb, k.tok + t, n, k.c0, p.D);
+      }
+      cp_async_commit();
+    }
+  };
   carry_begin(ch, sm.carry);
+  load(0);
   GateConst gc{both(0.f), both(0.f)};
   if (!GIVEN) gc = gate_const(p.A_log, p.dt_bias, c, p.D);
   float2 carry = read2(p.h0, k.row, c, p.D);  // before the round's first tile (warp 0's)
   bool lost = false;
+  Rows<TO> out;
+  out.begin(p.h, p.ldh, k.tok + k.rank * kTileT, k.c0, warp * kPer, 2 * lane);
   const int rounds = (k.chunks + ch.cs - 1) / ch.cs;
   for (int round = 0; round < rounds; ++round) {
-    cp_async_wait<0>();
+    const int n = length(round);
+    if (!ch.tma) {
+      cp_async_wait<0>();
+    } else if (n > 0 && !tc::mbar_wait(&sm.carry.loaded[round & 1], (round >> 1) & 1, nullptr, 0)) {
+      report_timeout(ch.status, 0x4c54);
+    }
     __syncthreads();  // the stage is complete, the other one free
     if (round + 1 < rounds) load(round + 1);
-    const int tt = round * ch.cs + k.rank;
-    const long long left = k.len - (long long)tt * kTileT;
-    const int n = left < kTileT ? (left < 0 ? 0 : (int)left) : kTileT;
     const FwdStage<TX, TG>& st = sm.stage[round & 1];
     const int mine = warp * kPer * kTileC + 2 * lane;
     float2 al[kPer], u[kPer];
-    float2 A = both(1.f), H = both(0.f);
 #pragma unroll
     for (int i0 = 0; i0 < kPer; i0 += kGroup) {
       float2 e[kGroup];
@@ -76,13 +94,21 @@ linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec) {
       for (int i = 0; i < kGroup; ++i) {
         al[i0 + i] = ex2_2(e[i]);
         u[i0 + i] = get2(st.x + mine + (i0 + i) * kTileC);
-        if (SCALE != kScaleNone)
-          u[i0 + i] = mul2(u[i0 + i], input_scale<SCALE>(e[i], al[i0 + i]));
       }
-      if (p.b)
+      if (SCALE != kScaleNone) {
+        float2 f[kGroup];
+        input_scales<SCALE, kGroup>(e, al + i0, f);
 #pragma unroll
-        for (int i = 0; i < kGroup; ++i)
-          u[i0 + i] = mul2(u[i0 + i], write_gate<GIVEN>(get2(st.b + mine + (i0 + i) * kTileC)));
+        for (int i = 0; i < kGroup; ++i) u[i0 + i] = mul2(u[i0 + i], f[i]);
+      }
+      if (p.b) {
+        float2 b[kGroup];
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) b[i] = get2(st.b + mine + (i0 + i) * kTileC);
+        write_gates<GIVEN, kGroup>(b);
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) u[i0 + i] = mul2(u[i0 + i], b[i]);
+      }
     }
     if (n < kTileT) {  // behind the sequence: the state passes through
 #pragma unroll
@@ -92,52 +118,49 @@ linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec) {
           u[i] = both(0.f);
         }
     }
+    float2 A = al[0], H = u[0];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
+    for (int i = 1; i < kPer; ++i) {
       H = fma2(al[i], H, u[i]);
       A = mul2(A, al[i]);
     }
     sm.carry.fold[warp][lane] = join4(A, H);
     __syncthreads();
-    A = both(1.f);  // what the tile's tokens before the warp's do
-    H = both(0.f);
     if (warp == 0) {
-      float2 tA = both(1.f), tH = both(0.f);
-#pragma unroll
+      A = both(1.f);
+      H = both(0.f);
+#pragma unroll 4
       for (int w = 0; w < kWarps; ++w) {
-        const float4 f = sm.carry.fold[w][lane];
-        tH = fma2(first2(f), tH, last2(f));
-        tA = mul2(tA, first2(f));
-      }
-      const float2 in = carry_round(ch, k.rank, round, join4(tA, tH), sm.carry, folds, &carry, &lost);
-      sm.carry.in[lane] = in;
-      if (n > 0) write2(p.states_out, k.chunk0 + tt, c, p.D, in);
-    } else {
-      for (int w = 0; w < warp; ++w) {
         const float4 f = sm.carry.fold[w][lane];
         H = fma2(first2(f), H, last2(f));
         A = mul2(A, first2(f));
       }
+      float2 v = carry_round(ch, k.rank, round, join4(A, H), sm.carry, folds, &carry, &lost);
+      if (n > 0) write2(p.states_out, k.chunk0 + round * ch.cs + k.rank, c, p.D, v);
+#pragma unroll 4
+      for (int w = 0; w < kWarps; ++w) {
+        sm.carry.start[w][lane] = v;
+        const float4 f = sm.carry.fold[w][lane];
+        v = fma2(first2(f), v, last2(f));
+      }
     }
     __syncthreads();
     if (p.h) {
-      float2 h = fma2(A, sm.carry.in[lane], H);
-      TO* out = static_cast<TO*>(p.h) + (k.tok + (long long)tt * kTileT + warp * kPer) * p.ldh + c;
-      if (n == kTileT && cols > 1 && (vec & 8)) {
+      float2 h = sm.carry.start[warp][lane];
+      if (n == kTileT && cols > 1 && vec) {
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           h = fma2(al[i], h, u[i]);
-          put2(out, h);
-          out += p.ldh;
+          put2(out.at(i), h);
         }
       } else {
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           h = fma2(al[i], h, u[i]);
-          if (warp * kPer + i < n) put2(out, h, cols);
-          out += p.ldh;
+          if (warp * kPer + i < n) put2(out.at(i), h, cols);
         }
       }
+      out.advance(step);
     }
   }
   if (k.rank == 0 && warp == 0) write2(p.ht, k.row, c, p.D, carry);
@@ -161,8 +184,17 @@ __global__ void __launch_bounds__(128) linrec_step_kernel(LinrecArgs p, float* s
   float2 e = take2<TG>(p.a, r * p.lda + c, cols);
   decay_exponents<GIVEN, 1>(&e, gc);
   const float2 al = ex2_2(e);
-  float2 u = mul2(take2<TX>(p.x, r * p.ldx + c, cols), input_scale<SCALE>(e, al));
-  if (p.b) u = mul2(u, write_gate<GIVEN>(take2<TG>(p.b, r * p.ldb + c, cols)));
+  float2 u = take2<TX>(p.x, r * p.ldx + c, cols);
+  if (SCALE != kScaleNone) {
+    float2 f;
+    input_scales<SCALE, 1>(&e, &al, &f);
+    u = mul2(u, f);
+  }
+  if (p.b) {
+    float2 b = take2<TG>(p.b, r * p.ldb + c, cols);
+    write_gates<GIVEN, 1>(&b);
+    u = mul2(u, b);
+  }
   const float2 st = fma2(al, read2(state, r, c, p.D), u);
   write2(state, r, c, p.D, st);
   put2(static_cast<TO*>(p.h) + r * p.ldh + c, st, cols);
@@ -207,11 +239,13 @@ struct FwdRun {
   template <typename TX, typename TG, bool GIVEN, int SCALE, bool WIDE>
   cudaError_t run() const {
     using TO = typename Wide<TX, WIDE>::type;
-    const int vec = rows16(p.x, p.ldx, sizeof(TX)) | rows16(p.a, p.lda, sizeof(TG)) << 1 |
-                    rows16(p.b, p.ldb, sizeof(TG)) << 2 | pairs(p.h, p.ldh, sizeof(TO)) << 3;
+    LinrecMaps maps;
+    Chains c = ch;
+    c.tma = map_tiles<TX>(&maps.x, p, p.x, p.ldx) && map_tiles<TG>(&maps.a, p, p.a, p.lda) &&
+            (!p.b || map_tiles<TG>(&maps.b, p, p.b, p.ldb));
     int cs = 1;
     return launch_chains(linrec_fwd_kernel<TX, TG, GIVEN, SCALE, TO>, sizeof(FwdSmem<TX, TG>), p,
-                         ch, vec, &cs, s);
+                         c, pairs(p.h, p.ldh, sizeof(TO)), &cs, s, maps);
   }
 };
 struct StepRun {

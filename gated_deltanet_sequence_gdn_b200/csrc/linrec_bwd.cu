@@ -12,10 +12,10 @@ namespace {
 
 template <typename TX, typename TG, typename TD>
 struct BwdStage {
-  alignas(16) TX x[kTileT * kTileC];
-  alignas(16) TG a[kTileT * kTileC];
-  alignas(16) TG b[kTileT * kTileC];
-  alignas(16) TD dh[kTileT * kTileC];
+  alignas(128) TX x[kTileT * kTileC];
+  alignas(128) TG a[kTileT * kTileC];
+  alignas(128) TG b[kTileT * kTileC];
+  alignas(128) TD dh[kTileT * kTileC];
 };
 template <typename TX, typename TG, typename TD>
 struct BwdSmem {
@@ -34,48 +34,77 @@ __device__ __forceinline__ void add_kept(float2* sum, float2* err, float2 v) {
 
 template <typename TX, typename TG, bool GIVEN, int SCALE, typename TD, typename TDG>
 __global__ void __launch_bounds__(kLinrecThreads, sizeof(TX) + sizeof(TG) + sizeof(TD) == 6 ? 2 : 1)
-linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const float* states, float2* sums) {
-  extern __shared__ __align__(16) unsigned char smem_raw[];
+linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ LinrecMaps maps,
+                  const float* states, float2* sums) {
+  extern __shared__ __align__(128) unsigned char smem_raw[];
   using Smem = BwdSmem<TX, TG, TD>;
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
   FoldRow* folds = reinterpret_cast<FoldRow*>(smem_raw + sizeof(Smem));
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, first = warp * kPer;
   const Chain k = chain_of(p, ch);
   const int c = k.c0 + 2 * lane, cols = p.D - c;
-  auto tile = [&](int round) { return k.chunks - 1 - (round * ch.cs + k.rank); };
-  auto tokens = [&](int tt) {
-    const long long left = k.len - (long long)tt * kTileT;
-    return tt < 0 ? 0 : left < kTileT ? (int)left : kTileT;
+  const int step = ch.cs * kTileT;
+  const int last = k.chunks - 1 - k.rank;  // the block's first tile; may be before the sequence
+  const long long tok0 = k.tok + last * (long long)kTileT;
+  const int tokens = (int)k.len - last * kTileT;  // from there to the sequence's end
+  auto tile = [&](int round) { return last - round * ch.cs; };
+  auto length = [&](int round) {  // of the round's tile: only the sequence's last is short
+    return tile(round) < 0 ? 0 : round == 0 && tokens < kTileT ? tokens : kTileT;
   };
   auto load = [&](int round) {
-    const int tt = tile(round), n = tokens(tt);
-    if (n > 0) {
-      const long long tok = k.tok + (long long)tt * kTileT;
-      BwdStage<TX, TG, TD>& st = sm.stage[round & 1];
-      load_tile(st.x, p.x, p.ldx, tok, n, k.c0, p.D, vec & 1);
-      load_tile(st.a, p.a, p.lda, tok, n, k.c0, p.D, vec & 2);
-      if (p.b) load_tile(st.b, p.b, p.ldb, tok, n, k.c0, p.D, vec & 4);
-      load_tile(st.dh, p.dh, p.lddh, tok, n, k.c0, p.D, vec & 8);
+    const int n = length(round), t = tile(round) * kTileT;
+    BwdStage<TX, TG, TD>& st = sm.stage[round & 1];
+    if (ch.tma) {
+      if (n > 0 && threadIdx.x == 0) {
+        uint64_t* bar = &sm.carry.loaded[round & 1];
+        const int y = ch.tab.cu ? (int)k.tok + t : t, z = ch.tab.cu ? 0 : k.row;
+        tc::mbar_arrive_expect_tx(bar, sizeof(st.x) + sizeof(st.a) + (p.b ? sizeof(st.b) : 0) +
+                                           sizeof(st.dh));
+        tma_load_3d(st.x, &maps.x, bar, k.c0, y, z);
+        tma_load_3d(st.a, &maps.a, bar, k.c0, y, z);
+        if (p.b) tma_load_3d(st.b, &maps.b, bar, k.c0, y, z);
+        tma_load_3d(st.dh, &maps.dh, bar, k.c0, y, z);
+      }
+    } else {
+      if (n > 0) {
+        load_elements(st.x, p.x, p.ldx, k.tok + t, n, k.c0, p.D);
+        load_elements(st.a, p.a, p.lda, k.tok + t, n, k.c0, p.D);
+        if (p.b) load_elements(st.b, p.b, p.ldb, k.tok + t, n, k.c0, p.D);
+        load_elements(st.dh, p.dh, p.lddh, k.tok + t, n, k.c0, p.D);
+      }
+      cp_async_commit();
     }
-    cp_async_commit();
   };
-  load(0);
   carry_begin(ch, sm.carry);
+  load(0);
   GateConst gc{both(0.f), both(0.f)};
   if (!GIVEN) gc = gate_const(p.A_log, p.dt_bias, c, p.D);
   float2 carry = read2(p.dht, k.row, c, p.D);  // behind the round's last tile (warp 0's)
   bool lost = false;
   float2 sA = both(0.f), eA = both(0.f), sb = both(0.f), eb = both(0.f);
+  Rows<TD> odx;
+  Rows<TDG> oda, odb;
+  odx.begin(p.dx, p.lddx, tok0, k.c0, first, 2 * lane);
+  oda.begin(p.da, p.ldda, tok0, k.c0, first, 2 * lane);
+  odb.begin(p.db, p.lddb, tok0, k.c0, first, 2 * lane);
   const int rounds = (k.chunks + ch.cs - 1) / ch.cs;
   for (int round = 0; round < rounds; ++round) {
-    const int tt = tile(round), n = tokens(tt);
-    cp_async_wait<0>();
+    const int tt = tile(round), n = length(round);
+    if (!ch.tma) {
+      cp_async_wait<0>();
+    } else if (n > 0 && !tc::mbar_wait(&sm.carry.loaded[round & 1], (round >> 1) & 1, nullptr, 0)) {
+      report_timeout(ch.status, 0x4c54);
+    }
     __syncthreads();  // the stage is complete, the other one free
     if (round + 1 < rounds) load(round + 1);
-    const BwdStage<TX, TG, TD>& st = sm.stage[round & 1];
+    BwdStage<TX, TG, TD>& st = sm.stage[round & 1];
+    if (n > 0 && n < kTileT && ch.tab.cu) {  // the next sequence's tokens
+      clear_rows(st.x, n);
+      tc::fence_proxy_async_smem();  // the stage's next tiles come by TMA
+      __syncthreads();
+    }
     const int mine = first * kTileC + 2 * lane;
     float2 al[kPer], be[kPer], f[kPer];
-    float2 hs = n > 0 ? read2(states, k.chunk0 + tt, c, p.D) : both(0.f);
     float2 A = both(1.f), H = both(0.f), R = both(0.f);
 #pragma unroll
     for (int i0 = 0; i0 < kPer; i0 += kGroup) {
@@ -86,9 +115,10 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const float* states, float2*
 #pragma unroll
       for (int i = 0; i < kGroup; ++i) {
         al[i0 + i] = ex2_2(e[i]);
-        f[i0 + i] = input_scale<SCALE>(e[i], al[i0 + i]);
-        be[i0 + i] = p.b ? write_gate<GIVEN>(get2(st.b + mine + (i0 + i) * kTileC)) : both(1.f);
+        be[i0 + i] = p.b ? get2(st.b + mine + (i0 + i) * kTileC) : both(1.f);
       }
+      input_scales<SCALE, kGroup>(e, al + i0, f + i0);
+      if (p.b) write_gates<GIVEN, kGroup>(be + i0);
     }
     if (n < kTileT) {  // behind the sequence: both states pass through
 #pragma unroll
@@ -113,23 +143,32 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const float* states, float2*
     sm.carry.fold[warp][lane] = join4(A, H);
     sm.back[warp][lane] = R;
     __syncthreads();
-    for (int w = 0; w < warp; ++w) {
-      const float4 q = sm.carry.fold[w][lane];
-      hs = fma2(first2(q), hs, last2(q));
-    }
-    A = both(1.f);  // what the tile's tokens after the warp's do to c
-    R = both(0.f);
-    for (int w = kWarps - 1; w > warp; --w) {
-      const float2 a = first2(sm.carry.fold[w][lane]);
-      R = fma2(a, R, sm.back[w][lane]);
-      A = mul2(A, a);
-    }
-    if (warp == 0) {  // with its own: the tile's
-      const float2 a = first2(sm.carry.fold[0][lane]);
-      const float4 own = join4(mul2(A, a), fma2(a, R, sm.back[0][lane]));
-      sm.carry.in[lane] = carry_round(ch, k.rank, round, own, sm.carry, folds, &carry, &lost);
+    if (warp == 0) {
+      float2 hs = n > 0 ? read2(states, k.chunk0 + tt, c, p.D) : both(0.f);
+      A = both(1.f);
+      R = both(0.f);
+#pragma unroll 4
+      for (int w = kWarps - 1; w >= 0; --w) {
+        const float2 a = first2(sm.carry.fold[w][lane]);
+        R = fma2(a, R, sm.back[w][lane]);
+        A = mul2(A, a);
+      }
+#pragma unroll 4
+      for (int w = 0; w < kWarps; ++w) {
+        sm.carry.start[w][lane] = hs;
+        const float4 q = sm.carry.fold[w][lane];
+        hs = fma2(first2(q), hs, last2(q));
+      }
+      float2 v = carry_round(ch, k.rank, round, join4(A, R), sm.carry, folds, &carry, &lost);
+#pragma unroll 4
+      for (int w = kWarps - 1; w >= 0; --w) {
+        const float2 r = sm.back[w][lane];
+        sm.back[w][lane] = v;
+        v = fma2(first2(sm.carry.fold[w][lane]), v, r);
+      }
     }
     __syncthreads();
+    float2 hs = sm.carry.start[warp][lane];
     float2 hp[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -138,10 +177,9 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const float* states, float2*
       if (SCALE != kScaleNone) u = mul2(u, f[i]);
       hs = fma2(al[i], hs, u);
     }
-    float2 cc = fma2(A, sm.carry.in[lane], R);
+    float2 cc = sm.back[warp][lane];
     float2 tA = both(0.f), tb = both(0.f);
-    const long long row = k.tok + (long long)tt * kTileT + first;
-    const bool whole = n == kTileT && cols > 1 && (vec & 0x70) == 0x70;
+    const bool whole = n == kTileT && cols > 1 && vec;
 #pragma unroll
     for (int i0 = kPer - kGroup; i0 >= 0; i0 -= kGroup) {
       float2 e[kGroup], slope[kGroup];
@@ -176,9 +214,9 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const float* states, float2*
           tA = add2(tA, make_float2(dg.x == 0.f ? 0.f : dg.x * e[j].x,
                                     dg.y == 0.f ? 0.f : dg.y * e[j].y));
         }
-        TD* px = static_cast<TD*>(p.dx) + (row + i) * p.lddx + c;
-        TDG* pa = static_cast<TDG*>(p.da) + (row + i) * p.ldda + c;
-        TDG* pb = static_cast<TDG*>(p.db) + (row + i) * p.lddb + c;
+        TD* px = odx.at(i);
+        TDG* pa = oda.at(i);
+        TDG* pb = odb.at(i);
         if (whole) {
           put2(px, dx);
           put2(pa, da);
@@ -190,6 +228,9 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const float* states, float2*
         }
       }
     }
+    odx.advance(-step);
+    oda.advance(-step);
+    odb.advance(-step);
     if (!GIVEN) {  // a lane keeps its channels: their sums run through the rounds
       add_kept(&sA, &eA, tA);
       add_kept(&sb, &eb, tb);
@@ -251,13 +292,17 @@ struct BwdRun {
   cudaError_t run() const {
     using TD = typename Wide<TX, WIDE>::type;
     using TDG = typename Wide<TD, GIVEN>::type;
-    const int vec = rows16(p.x, p.ldx, sizeof(TX)) | rows16(p.a, p.lda, sizeof(TG)) << 1 |
-                    rows16(p.b, p.ldb, sizeof(TG)) << 2 | rows16(p.dh, p.lddh, sizeof(TD)) << 3 |
-                    pairs(p.dx, p.lddx, sizeof(TD)) << 4 | pairs(p.da, p.ldda, sizeof(TDG)) << 5 |
-                    pairs(p.db, p.lddb, sizeof(TDG)) << 6;
+    LinrecMaps maps;
+    Chains c = ch;
+    c.tma = map_tiles<TX>(&maps.x, p, p.x, p.ldx) && map_tiles<TG>(&maps.a, p, p.a, p.lda) &&
+            (!p.b || map_tiles<TG>(&maps.b, p, p.b, p.ldb)) &&
+            map_tiles<TD>(&maps.dh, p, p.dh, p.lddh);
+    const int vec = pairs(p.dx, p.lddx, sizeof(TD)) && pairs(p.da, p.ldda, sizeof(TDG)) &&
+                    pairs(p.db, p.lddb, sizeof(TDG));
     int cs = 1;
     cudaError_t e = launch_chains(linrec_bwd_kernel<TX, TG, GIVEN, SCALE, TD, TDG>,
-                                  sizeof(BwdSmem<TX, TG, TD>), p, ch, vec, &cs, s, states, sums);
+                                  sizeof(BwdSmem<TX, TG, TD>), p, c, vec, &cs, s, maps, states,
+                                  sums);
     if (e != cudaSuccess || GIVEN) return e;
     linrec_sums_kernel<<<(p.D + 31) / 32, dim3(32, kSumRows), 0, s>>>(
         sums, (long long)p.B * cs, p.D, p.dA_log, p.ddt_bias);

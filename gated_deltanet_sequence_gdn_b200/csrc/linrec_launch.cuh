@@ -18,10 +18,23 @@ cudaError_t make_chains(const LinrecArgs& a, void* workspace, bool table, cudaSt
 cudaError_t launch_linrec_scan(const LinrecArgs& a, const Chains& ch, int wide_flag,
                                cudaStream_t s);
 
-// Rows that start on 16 bytes; rows whose element pairs are aligned.
-inline int rows16(const void* p, long long ld, int es) {
-  return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(ld * es)) & 15) == 0;
+// The map of a tensor's tiles, where its rows start on 16 bytes.
+template <typename T>
+bool map_tiles(CUtensorMap* m, const LinrecArgs& p, const void* base, long long ld) {
+  if (((reinterpret_cast<uintptr_t>(base) | (uintptr_t)(ld * (long long)sizeof(T))) & 15) != 0)
+    return false;
+  auto enc = tensor_map_encoder();
+  if (enc == nullptr) return false;
+  const cuuint64_t rows = p.cu ? 1 : p.B;
+  const cuuint64_t dims[3] = {(cuuint64_t)p.D, (cuuint64_t)p.T, rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)ld * sizeof(T), (cuuint64_t)p.T * ld * sizeof(T)};
+  const cuuint32_t box[3] = {kTileC, kTileT, 1}, es[3] = {1, 1, 1};
+  return enc(m, sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+             3, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+// Element pairs that are aligned.
 inline int pairs(const void* p, long long ld, int es) {
   return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(ld * es)) & (2 * es - 1)) == 0;
 }

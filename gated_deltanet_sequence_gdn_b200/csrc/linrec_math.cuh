@@ -35,30 +35,12 @@ __device__ __forceinline__ float sqrt_f(float x) {
   return y;
 }
 
-// Two floats in one 64-bit register pair.
-union F2 {
-  unsigned long long u;
-  float2 f;
-};
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  F2 x, y, z, r;
-  x.f = a; y.f = b; z.f = c;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.u) : "l"(x.u), "l"(y.u), "l"(z.u));
-  return r.f;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  F2 x, y, r;
-  x.f = a; y.f = b;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(x.u), "l"(y.u));
-  return r.f;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  F2 x, y, r;
-  x.f = a; y.f = b;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(x.u), "l"(y.u));
-  return r.f;
-}
+// Two floats at a time.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 held(float v) { return make_float2(v, v); }
 __device__ __forceinline__ float2 ex2_2(float2 x) { return make_float2(ex2_f(x.x), ex2_f(x.y)); }
 __device__ __forceinline__ float2 rcp_2(float2 x) { return make_float2(rcp_f(x.x), rcp_f(x.y)); }
 
@@ -70,27 +52,42 @@ __device__ __forceinline__ void log1p_over(const float2* y, float2* p) {
   const float k[9] = {5.232694263e-03f, -2.950523877e-02f, 7.822595187e-02f,
                       -1.366324579e-01f, 1.910600676e-01f, -2.484298221e-01f,
                       3.331909681e-01f, -4.999949314e-01f, 9.999999699e-01f};
+  const float2 k0 = held(k[0]), k1 = held(k[1]);
 #pragma unroll
-  for (int i = 0; i < N; ++i) p[i] = fma2(y[i], both(k[0]), both(k[1]));
+  for (int i = 0; i < N; ++i) p[i] = fma2(y[i], k0, k1);
 #pragma unroll
-  for (int j = 2; j < 9; ++j)
+  for (int j = 2; j < 9; ++j) {
+    const float2 kj = held(k[j]);
 #pragma unroll
-    for (int i = 0; i < N; ++i) p[i] = fma2(p[i], y[i], both(k[j]));
+    for (int i = 0; i < N; ++i) p[i] = fma2(p[i], y[i], kj);
+  }
 }
 
-// 1 - 2^e for e <= 0: the exponential's series in v = e ln 2 where the difference would
+// f[i] = 1 - 2^e for e <= 0: the exponential's series in v = e ln 2 where the difference would
 // cancel (v > -0.35: the first term left out is v^7 / 8! < 2e-8 relative), 1 - pow elsewhere
 // (pow = 2^e).
-__device__ __forceinline__ float2 one_minus_ex2(float2 e, float2 pow) {
-  const float2 v = mul2(e, both(kLn2));
-  float2 p = fma2(v, both(1.f / 5040.f), both(1.f / 720.f));
-  p = fma2(v, p, both(1.f / 120.f));
-  p = fma2(v, p, both(1.f / 24.f));
-  p = fma2(v, p, both(1.f / 6.f));
-  p = fma2(v, p, both(0.5f));
-  p = fma2(v, p, both(1.f));
-  p = mul2(v, p);
-  return make_float2(e.x > -0.5f ? -p.x : 1.f - pow.x, e.y > -0.5f ? -p.y : 1.f - pow.y);
+template <int N>
+__device__ __forceinline__ void one_minus_ex2(const float2* e, const float2* pow, float2* f) {
+  float2 v[N];
+  const float2 ln2 = held(kLn2), k0 = held(-1.f / 5040.f), k1 = held(-1.f / 720.f);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    v[i] = mul2(e[i], ln2);
+    f[i] = fma2(v[i], k0, k1);
+  }
+  const float k[5] = {-1.f / 120.f, -1.f / 24.f, -1.f / 6.f, -0.5f, -1.f};
+#pragma unroll
+  for (int j = 0; j < 5; ++j) {
+    const float2 kj = held(k[j]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = fma2(v[i], f[i], kj);
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    f[i] = mul2(v[i], f[i]);
+    if (!(e[i].x > -0.5f)) f[i].x = 1.f - pow[i].x;
+    if (!(e[i].y > -0.5f)) f[i].y = 1.f - pow[i].y;
+  }
 }
 
 // Per-channel constants of the gates.
@@ -139,12 +136,12 @@ template <int N>
 __device__ __forceinline__ void decay_exponents_slope(float2* a, const GateConst& k,
                                                       float2* slope) {
   float2 y[N], q[N];
-  const float2 rate = mul2(k.rate, both(kLn2));
+  const float2 rate = mul2(k.rate, both(kLn2)), one = held(1.f);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     a[i] = add2(a[i], k.bias);
     y[i] = make_float2(ex2_f(-fabsf(a[i].x) * kLog2e), ex2_f(-fabsf(a[i].y) * kLog2e));
-    const float2 r = rcp_2(add2(y[i], both(1.f)));
+    const float2 r = rcp_2(add2(y[i], one));
     slope[i] = mul2(rate, make_float2(a[i].x >= 0.f ? r.x : r.x * y[i].x,
                                       a[i].y >= 0.f ? r.y : r.y * y[i].y));
   }
@@ -156,15 +153,25 @@ __device__ __forceinline__ void decay_exponents_slope(float2* a, const GateConst
   }
 }
 
-// The input scale f from alpha = 2^e.
-template <int SCALE>
-__device__ __forceinline__ float2 input_scale(float2 e, float2 alpha) {
-  if (SCALE == kScaleTied) return one_minus_ex2(e, alpha);
-  if (SCALE == kScaleUnit) {
-    const float2 q = one_minus_ex2(add2(e, e), mul2(alpha, alpha));
-    return make_float2(sqrt_f(q.x), sqrt_f(q.y));
+// The input scales f of N tokens from alpha = 2^e.
+template <int SCALE, int N>
+__device__ __forceinline__ void input_scales(const float2* e, const float2* alpha, float2* f) {
+  if (SCALE == kScaleTied) {
+    one_minus_ex2<N>(e, alpha, f);
+  } else if (SCALE == kScaleUnit) {
+    float2 e2[N], a2[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      e2[i] = add2(e[i], e[i]);
+      a2[i] = mul2(alpha[i], alpha[i]);
+    }
+    one_minus_ex2<N>(e2, a2, f);
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = make_float2(sqrt_f(f[i].x), sqrt_f(f[i].y));
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = both(1.f);
   }
-  return both(1.f);
 }
 // df/dg.  sqrt(1 - alpha^2) has an infinite slope at g = 0; what reaches a is f' dg/da, which
 // goes to 0 there with softplus, so f' is taken as 0 where f underflows.
@@ -175,17 +182,20 @@ __device__ __forceinline__ float input_scale_slope(float alpha, float f) {
   return 0.f;
 }
 
-// beta; GIVEN: b is beta itself.
-template <bool GIVEN>
-__device__ __forceinline__ float2 write_gate(float2 b) {
-  if (GIVEN) return b;
-  return rcp_2(add2(ex2_2(mul2(b, both(-kLog2e))), both(1.f)));
+// beta[i] in place of b[i]; GIVEN: b is beta itself.
+template <bool GIVEN, int N>
+__device__ __forceinline__ void write_gates(float2* b) {
+  if (GIVEN) return;
+  const float2 one = held(1.f);
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    b[i] = rcp_2(add2(make_float2(ex2_f(b[i].x * -kLog2e), ex2_f(b[i].y * -kLog2e)), one));
 }
 // 1 - beta = beta e^{-b}, without the cancellation (the exponent is kept below 2^126, where
 // beta has underflowed).
 __device__ __forceinline__ float2 write_gate_rest(float2 b, float2 beta) {
-  const float2 e = mul2(b, both(-kLog2e));
-  return mul2(beta, make_float2(ex2_f(fminf(e.x, 126.f)), ex2_f(fminf(e.y, 126.f))));
+  return mul2(beta, make_float2(ex2_f(fminf(b.x * -kLog2e, 126.f)),
+                                ex2_f(fminf(b.y * -kLog2e, 126.f))));
 }
 
 }  // namespace gdn

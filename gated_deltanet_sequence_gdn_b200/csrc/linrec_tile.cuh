@@ -18,6 +18,7 @@
 #include "linrec.cuh"
 #include "linrec_math.cuh"
 #include "tc_ptx.cuh"
+#include "tmap.cuh"
 
 namespace gdn {
 
@@ -35,6 +36,11 @@ struct SeqTab {
   const int* chunk0;
 };
 
+// Maps of the inputs' tiles.
+struct LinrecMaps {
+  CUtensorMap x, a, b, dh;
+};
+
 // One launch: the chains by cluster, row by row of the batch.
 struct Chains {
   SeqTab tab;
@@ -43,6 +49,7 @@ struct Chains {
   int* status;
   unsigned spin;  // polls before a wait gives up
   bool fault;     // test hook: the first block of a cluster keeps its folds to itself
+  bool tma;       // the inputs come by TMA
 };
 
 // One chain, as a block of its cluster sees it.
@@ -75,9 +82,10 @@ __device__ __forceinline__ Chain chain_of(const LinrecArgs& p, const Chains& ch)
 // Shared memory of the carry: each warp's fold, the carry into the tile, and behind the
 // kernel's own shared memory the cluster's folds, [2 rounds][cs][32].
 struct CarrySmem {
-  float4 fold[kWarps][32];  // (A, A', H, H') of a lane's two channels
-  float2 in[32];
-  uint64_t full[2];  // the round's folds have arrived
+  float4 fold[kWarps][32];   // (A, A', H, H') of a lane's two channels
+  float2 start[kWarps][32];  // what enters each warp's tokens
+  uint64_t full[2];          // the round's folds have arrived
+  uint64_t loaded[2];        // the stage's tiles have
 };
 using FoldRow = float4[32];
 
@@ -133,9 +141,11 @@ __device__ __forceinline__ void carry_begin(const Chains& ch, CarrySmem& sm) {
   if (threadIdx.x == 0) {
     tc::mbar_init(&sm.full[0], 1);
     tc::mbar_init(&sm.full[1], 1);
+    tc::mbar_init(&sm.loaded[0], 1);
+    tc::mbar_init(&sm.loaded[1], 1);
     tc::fence_mbar_init();
   }
-  __syncwarp();
+  __syncthreads();
   if (ch.cs > 1) tc::cluster_sync();  // the barriers are there before a peer counts on them
 }
 // No block leaves while a peer may still send to it.
@@ -144,11 +154,19 @@ __device__ __forceinline__ void carry_end(const Chains& ch) {
   if (ch.cs > 1) tc::cluster_sync();
 }
 
-__device__ __forceinline__ void cp_async16(void* dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(dst)),
-               "l"(src), "r"(bytes)
-               : "memory");
+// Tiles of one tensor to shared memory [64][64].  Tensors whose rows start on 16 bytes come
+// by TMA, one instruction a tile, through a map over [channels][tokens][rows of the batch]
+// (zeros behind the last token of a dense row and behind the last channel); the tokens behind
+// a packed sequence are the next one's and are cleared by the caller.
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, uint64_t* bar, int c0,
+                                            int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(tc::smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(tc::smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
 }
+// The others by element: asynchronous copies of 4 bytes, or plain loads of 2.
 __device__ __forceinline__ void cp_async4(void* dst, const void* src, int bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(tc::smem_u32(dst)), "l"(src),
                "r"(bytes)
@@ -161,47 +179,25 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-
-// `n` tokens of one tensor from row `tok` on to shared memory [64][64], zeros behind them and
-// behind the last channel; `vec`: rows start on 16 bytes and move in 16-byte pieces.
 template <typename T>
-__device__ __forceinline__ void load_tile(T* dst, const void* base, long long ld, long long tok,
-                                          int n, int c0, int D, bool vec) {
+__device__ __forceinline__ void load_elements(T* dst, const void* base, long long ld,
+                                              long long tok, int n, int c0, int D) {
   const T* src = static_cast<const T*>(base) + tok * ld + c0;
-  const int cols = D - c0 < kTileC ? D - c0 : kTileC;
-  if (vec) {
-    constexpr int E = 16 / sizeof(T), P = kTileC / E;  // elements of a piece, pieces of a row
-    constexpr int kRows = kLinrecThreads / P;          // rows of a step
-    const int r0 = threadIdx.x / P, c = (threadIdx.x % P) * E;
-    const int left = cols - c, bytes = (left < 0 ? 0 : left < E ? left : E) * (int)sizeof(T);
-    src += r0 * ld + c;
-    dst += r0 * kTileC + c;
-    if (n == kTileT && bytes == 16) {
-#pragma unroll
-      for (int i = 0; i < kTileT / kRows; ++i) {
-        cp_async16(dst + i * kRows * kTileC, src, 16);
-        src += kRows * ld;
-      }
-      return;
-    }
-#pragma unroll
-    for (int i = 0; i < kTileT / kRows; ++i) {
-      const int in = r0 + i * kRows < n ? bytes : 0;
-      cp_async16(dst + i * kRows * kTileC, in ? static_cast<const void*>(src) : base, in);
-      src += kRows * ld;
-    }
-  } else {
 #pragma unroll 4
-    for (int i = 0; i < kTileT * kTileC / kLinrecThreads; ++i) {
-      const int k = threadIdx.x + i * kLinrecThreads, r = k / kTileC, c = k % kTileC;
-      const bool in = r < n && c < cols;
-      if (sizeof(T) == 4)
-        cp_async4(dst + r * kTileC + c, in ? static_cast<const void*>(src + r * ld + c) : base,
-                  in ? 4 : 0);
-      else
-        dst[r * kTileC + c] = in ? src[r * ld + c] : from_f32<T>(0.f);
-    }
+  for (int i = 0; i < kTileT * kTileC / kLinrecThreads; ++i) {
+    const int k = threadIdx.x + i * kLinrecThreads, r = k / kTileC, c = k % kTileC;
+    const bool in = r < n && c < D - c0;
+    if (sizeof(T) == 4)
+      cp_async4(dst + k, in ? src + r * ld + c : src, in ? 4 : 0);
+    else
+      dst[k] = in ? src[r * ld + c] : from_f32<T>(0.f);
   }
+}
+// Clears the rows of a tile behind its n tokens.
+template <typename T>
+__device__ __forceinline__ void clear_rows(T* tile, int n) {
+  for (int i = n * kTileC + threadIdx.x; i < kTileT * kTileC; i += kLinrecThreads)
+    tile[i] = from_f32<T>(0.f);
 }
 
 // A lane's two channels.
@@ -220,6 +216,23 @@ __device__ __forceinline__ void put2(T* p, float2 v, int cols) {
   if (cols > 0) p[0] = from_f32<T>(v.x);
   if (cols > 1) p[1] = from_f32<T>(v.y);
 }
+// An output tensor of a block: a 64-bit base that moves from tile to tile, the same for all
+// threads, and 32-bit byte offsets inside a tile (64 rows of at most 2^23 elements).
+template <typename T>
+struct Rows {
+  char* base;
+  uint32_t off, ld;  // bytes: of the thread's first element, from token to token
+  __device__ __forceinline__ void begin(void* p, long long row_elems, long long tok, int c0,
+                                        int first, int lane2) {
+    base = static_cast<char*>(p) + (tok * row_elems + c0) * (long long)sizeof(T);
+    ld = (uint32_t)row_elems * (uint32_t)sizeof(T);
+    off = (uint32_t)first * ld + (uint32_t)lane2 * (uint32_t)sizeof(T);
+  }
+  __device__ __forceinline__ T* at(int i) const {
+    return reinterpret_cast<T*>(base + (off + (uint32_t)i * ld));
+  }
+  __device__ __forceinline__ void advance(int tokens) { base += (long long)tokens * ld; }
+};
 // Two floats of a [.., D] array at channel c (0 outside, or where the array is NULL).
 __device__ __forceinline__ float2 read2(const float* base, long long row, int c, int D) {
   if (base == nullptr) return both(0.f);
