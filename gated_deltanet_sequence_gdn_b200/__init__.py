@@ -648,9 +648,9 @@ def _on_device(fn):
     device's current stream); what it allocates then belongs to that stream."""
     @functools.wraps(fn)
     def call(first, *args, stream=None, **kw):
-        if not first.is_cuda:
-            raise ValueError("tensor must live on a CUDA device")
         dev = first.device
+        if dev.type != "cuda":
+            raise ValueError("tensor must live on a CUDA device")
         if stream is None and dev.index == torch.cuda.current_device():
             return fn(first, *args, **kw)
         if stream is not None and stream.device != dev:
@@ -660,16 +660,26 @@ def _on_device(fn):
     return call
 
 
-def _dense(t, dtype, shape, dev, name):
-    """Pointer of a contiguous tensor of this dtype, shape and device (None -> NULL)."""
-    if t is None:
-        return None
-    if t.dtype != dtype:
+def _here(dev):
+    """The handle of a device's current stream."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _like(t, dtype, shape, dev, name):
+    """Raises unless the tensor has this dtype, shape and device."""
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != dev:
         raise ValueError(f"{name}: on {t.device}, expected {dev}")
+
+
+def _dense(t, dtype, shape, dev, name):
+    """Pointer of a contiguous tensor of this dtype, shape and device (None -> NULL)."""
+    if t is None:
+        return None
+    _like(t, dtype, shape, dev, name)
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
     return t.data_ptr()
@@ -681,21 +691,18 @@ def _strided(t, dtype, shape, dev, name, tail=1):
     token's elements (None -> (NULL, 0))."""
     if t is None:
         return None, 0
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name}: on {t.device}, expected {dev}")
-    st, n = t.stride(), t.dim()
-    row = 1
-    for i in range(n - 1, n - 1 - tail, -1):
-        if shape[i] > 1 and st[i] != row:
+    _like(t, dtype, shape, dev, name)
+    row = shape[-1] if tail == 1 else shape[-1] * shape[-2]
+    if t.is_contiguous():
+        return t.data_ptr(), row
+    st, lead = t.stride(), t.dim() - tail
+    inner = 1
+    for i in range(t.dim() - 1, lead - 1, -1):
+        if shape[i] > 1 and st[i] != inner:
             raise ValueError(f"{name}: the elements of a token must be contiguous")
-        row *= shape[i]
+        inner *= shape[i]
     ld = row
     if t.numel() > 0:
-        lead = n - tail
         if shape[lead - 1] > 1:
             ld = st[lead - 1]
             if lead == 2 and shape[0] > 1 and st[0] != ld * shape[1]:
@@ -798,10 +805,10 @@ def gdn_linrec_fwd(x, a, b=None, A_log=None, dt_bias=None, h0=None, *, cu_seqlen
     dev, f32 = x.device, torch.float32
     odt = f32 if out_f32 else x.dtype
     if h is None:
-        h = torch.empty(x.shape, device=dev, dtype=odt)
+        h = x.new_empty(x.shape, dtype=odt)
     ph, ldh = _strided(h, odt, x.shape, dev, "h")
     if ht is None and want_ht:
-        ht = torch.empty((B, D), device=dev, dtype=f32)
+        ht = x.new_empty((B, D), dtype=f32)
     if want_states or states is not None:
         shape = (gdn_linrec_chunks(B, T, cu), D)
         if states is None:
@@ -810,12 +817,13 @@ def gdn_linrec_fwd(x, a, b=None, A_log=None, dt_bias=None, h0=None, *, cu_seqlen
         ps = _dense(states, f32, shape, dev, "states")
     else:
         ps = None
-    keep, ws, ws_bytes = _workspace(
-        workspace, lib.gdn_linrec_workspace_bytes(cu, B, T, D), dev)
+    # a dense batch needs none
+    need = 0 if cu is None else lib.gdn_linrec_workspace_bytes(cu, B, T, D)
+    keep, ws, ws_bytes = _workspace(workspace, need, dev)
     _check(lib.gdn_linrec_fwd(*ins, _dense(h0, f32, (B, D), dev, "h0"), cu, B, T, D, *lds,
                               _dtype_code(x.dtype), flags | (OUT_F32 if out_f32 else 0), ph, ldh,
                               _dense(ht, f32, (B, D), dev, "ht"), ps, ws, ws_bytes,
-                              torch.cuda.current_stream().cuda_stream), "gdn_linrec_fwd")
+                              _here(dev)), "gdn_linrec_fwd")
     return (h, ht, states) if want_states else (h, ht)
 
 
@@ -835,14 +843,13 @@ def gdn_linrec_bwd(x, a, b, A_log, dt_bias, h0, dh, dht=None, *, cu_seqlens=None
     ddt = f32 if grad_f32 else x.dtype
     gdt = f32 if gates_precomputed else ddt
     pdh, lddh = _strided(dh, ddt, x.shape, dev, "dh")
-    out = {"dx": torch.empty(x.shape, device=dev, dtype=ddt),
-           "da": torch.empty(x.shape, device=dev, dtype=gdt),
-           "db": None if b is None else torch.empty(x.shape, device=dev, dtype=gdt),
+    out = {"dx": x.new_empty(x.shape, dtype=ddt), "da": x.new_empty(x.shape, dtype=gdt),
+           "db": None if b is None else x.new_empty(x.shape, dtype=gdt),
            "dA_log": None, "ddt_bias": None,
-           "dh0": torch.empty((B, D), device=dev, dtype=f32) if want_dh0 else None}
+           "dh0": x.new_empty((B, D), dtype=f32) if want_dh0 else None}
     if not gates_precomputed:
-        out["dA_log"] = torch.empty((D,), device=dev, dtype=f32)
-        out["ddt_bias"] = torch.empty((D,), device=dev, dtype=f32)
+        out["dA_log"] = x.new_empty((D,), dtype=f32)
+        out["ddt_bias"] = x.new_empty((D,), dtype=f32)
     ps = None
     if states is not None:
         ps = _dense(states, f32, (gdn_linrec_chunks(B, T, cu), D), dev, "states")
@@ -855,7 +862,7 @@ def gdn_linrec_bwd(x, a, b, A_log, dt_bias, h0, dh, dht=None, *, cu_seqlens=None
                               _dtype_code(x.dtype), flags | (GRAD_F32 if grad_f32 else 0),
                               ptr["dx"], D, ptr["da"], D, ptr["db"], D, ptr["dA_log"],
                               ptr["ddt_bias"], ptr["dh0"], ws, ws_bytes,
-                              torch.cuda.current_stream().cuda_stream), "gdn_linrec_bwd")
+                              _here(dev)), "gdn_linrec_bwd")
     return out
 
 
@@ -870,12 +877,11 @@ def gdn_linrec_step(x, a, b, A_log, dt_bias, state, *, input_scale="none",
     ins, lds, flags = _linrec_inputs(x, a, b, A_log, dt_bias, gates_precomputed, input_scale)
     odt = torch.float32 if out_f32 else x.dtype
     if h is None:
-        h = torch.empty((N, D), device=x.device, dtype=odt)
+        h = x.new_empty((N, D), dtype=odt)
     ph, ldh = _strided(h, odt, (N, D), x.device, "h")
     _check(lib.gdn_linrec_step(*ins, _dense(state, torch.float32, (N, D), x.device, "state"), N,
                                D, *lds, _dtype_code(x.dtype), flags | (OUT_F32 if out_f32 else 0),
-                               ph, ldh, torch.cuda.current_stream().cuda_stream),
-           "gdn_linrec_step")
+                               ph, ldh, _here(x.device)), "gdn_linrec_step")
     return h
 
 
@@ -924,13 +930,13 @@ def _rope_fwd(_, q, k, positions, inv_freq, q_weight, k_weight, norm, eps, scale
     args, flags, dt, dev, lead = _rope_inputs(q, k, positions, inv_freq, q_weight, k_weight,
                                               norm, interleaved)
     if q is not None and q_out is None:
-        q_out = torch.empty(q.shape, device=dev, dtype=dt)
+        q_out = q.new_empty(q.shape)
     if k is not None and k_out is None:
-        k_out = torch.empty(k.shape, device=dev, dtype=dt)
+        k_out = k.new_empty(k.shape)
     po = _strided(q_out, dt, () if q is None else q.shape, dev, "q_out", 2)
     ko = _strided(k_out, dt, () if k is None else k.shape, dev, "k_out", 2)
     _check(lib.gdn_qk_norm_rope(*args, _dtype_code(dt), flags, eps, scale, *po, *ko,
-                                torch.cuda.current_stream().cuda_stream), "gdn_qk_norm_rope")
+                                _here(dev)), "gdn_qk_norm_rope")
     return q_out, k_out
 
 
@@ -959,10 +965,10 @@ def _rope_bwd(_, q, k, positions, inv_freq, q_weight, k_weight, dq_out, dk_out, 
     gdt = torch.float32 if grad_f32 else dt
     gq = _strided(dq_out, gdt, () if q is None else q.shape, dev, "dq_out", 2)
     gk = _strided(dk_out, gdt, () if k is None else k.shape, dev, "dk_out", 2)
-    out = {"dq": None if q is None else torch.empty(q.shape, device=dev, dtype=gdt),
-           "dk": None if k is None else torch.empty(k.shape, device=dev, dtype=gdt)}
+    out = {"dq": None if q is None else q.new_empty(q.shape, dtype=gdt),
+           "dk": None if k is None else k.new_empty(k.shape, dtype=gdt)}
     for name, w in (("dq_weight", q_weight), ("dk_weight", k_weight)):
-        out[name] = None if w is None else torch.empty((d,), device=dev, dtype=torch.float32)
+        out[name] = None if w is None else torch.empty_like(w)
     need = 0
     if q_weight is not None or k_weight is not None:
         need = lib.gdn_qk_norm_rope_bwd_workspace_bytes(tokens, Hq, Hk, d, flags)
@@ -972,8 +978,7 @@ def _rope_bwd(_, q, k, positions, inv_freq, q_weight, k_weight, dq_out, dk_out, 
                                     flags | (GRAD_F32 if grad_f32 else 0), eps, scale,
                                     ptr["dq"], Hq * d, ptr["dk"], Hk * d, ptr["dq_weight"],
                                     ptr["dk_weight"], ws, ws_bytes,
-                                    torch.cuda.current_stream().cuda_stream),
-           "gdn_qk_norm_rope_bwd")
+                                    _here(dev)), "gdn_qk_norm_rope_bwd")
     return out
 
 

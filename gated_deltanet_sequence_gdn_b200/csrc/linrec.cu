@@ -243,9 +243,10 @@ struct FwdRun {
     Chains c = ch;
     c.tma = map_tiles<TX>(&maps.x, p, p.x, p.ldx) && map_tiles<TG>(&maps.a, p, p.a, p.lda) &&
             (!p.b || map_tiles<TG>(&maps.b, p, p.b, p.ldb));
+    static KernelSlots known;
     int cs = 1;
     return launch_chains(linrec_fwd_kernel<TX, TG, GIVEN, SCALE, TO>, sizeof(FwdSmem<TX, TG>), p,
-                         c, pairs(p.h, p.ldh, sizeof(TO)), &cs, s, maps);
+                         c, &known, pairs(p.h, p.ldh, sizeof(TO)), &cs, s, maps);
   }
 };
 struct StepRun {

@@ -248,9 +248,14 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
         vA = add2(vA, first2(q));
         vb = add2(vb, last2(q));
       }
-      float2* to = sums + ((long long)k.row * ch.cs + k.rank) * p.D + c;
-      if (cols > 0) to[0] = make_float2(vA.x, vb.x);
-      if (cols > 1) to[1] = make_float2(vA.y, vb.y);
+      if (sums == nullptr) {  // the only block of its channels
+        write2(p.dA_log, 0, c, p.D, vA);
+        write2(p.ddt_bias, 0, c, p.D, vb);
+      } else {
+        float2* to = sums + ((long long)k.row * ch.cs + k.rank) * p.D + c;
+        if (cols > 0) to[0] = make_float2(vA.x, vb.x);
+        if (cols > 1) to[1] = make_float2(vA.y, vb.y);
+      }
     }
   }
   carry_end(ch);
@@ -297,13 +302,15 @@ struct BwdRun {
     c.tma = map_tiles<TX>(&maps.x, p, p.x, p.ldx) && map_tiles<TG>(&maps.a, p, p.a, p.lda) &&
             (!p.b || map_tiles<TG>(&maps.b, p, p.b, p.ldb)) &&
             map_tiles<TD>(&maps.dh, p, p.dh, p.lddh);
+    const bool alone = p.B == 1 && most_blocks(p) == 1;  // one block a channel: no sums to join
     const int vec = pairs(p.dx, p.lddx, sizeof(TD)) && pairs(p.da, p.ldda, sizeof(TDG)) &&
                     pairs(p.db, p.lddb, sizeof(TDG));
+    static KernelSlots known;
     int cs = 1;
     cudaError_t e = launch_chains(linrec_bwd_kernel<TX, TG, GIVEN, SCALE, TD, TDG>,
-                                  sizeof(BwdSmem<TX, TG, TD>), p, c, vec, &cs, s, maps, states,
-                                  sums);
-    if (e != cudaSuccess || GIVEN) return e;
+                                  sizeof(BwdSmem<TX, TG, TD>), p, c, &known, vec, &cs, s, maps,
+                                  states, alone ? nullptr : sums);
+    if (e != cudaSuccess || GIVEN || alone) return e;
     linrec_sums_kernel<<<(p.D + 31) / 32, dim3(32, kSumRows), 0, s>>>(
         sums, (long long)p.B * cs, p.D, p.dA_log, p.ddt_bias);
     return cudaGetLastError();

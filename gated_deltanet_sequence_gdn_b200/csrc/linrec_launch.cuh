@@ -2,6 +2,8 @@
 // recurrence: workspace layout, choice of the kernel by type, the launch.
 #pragma once
 
+#include <atomic>
+
 #include "linrec_tile.cuh"
 
 namespace gdn {
@@ -60,12 +62,19 @@ inline int cluster_size(const LinrecArgs& p, long long chains, int slots) {
   return cs;
 }
 
-template <typename K, typename... More>
-cudaError_t launch_chains(K kernel, size_t smem, const LinrecArgs& p, const Chains& chains,
-                          int vec, int* cluster, cudaStream_t s, More... more) {
+// What the runtime says of one kernel on this device, asked once: blocks that run at once
+// (0: not asked yet).
+struct KernelSlots {
+  std::atomic<int> at[64];
+};
+template <typename K>
+cudaError_t kernel_slots(K kernel, size_t smem, KernelSlots* known, int* slots) {
   int dev = 0, sms = 0, per = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const bool keep = dev < 64;
+  if (keep && (*slots = known->at[dev].load(std::memory_order_acquire)) != 0) return cudaSuccess;
+  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const size_t most = smem + 2 * kMaxCluster * sizeof(FoldRow);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
@@ -74,9 +83,21 @@ cudaError_t launch_chains(K kernel, size_t smem, const LinrecArgs& p, const Chai
   if (e == cudaSuccess)
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kLinrecThreads, smem);
   if (e != cudaSuccess) return e;
+  *slots = sms * (per > 0 ? per : 1);
+  if (keep) known->at[dev].store(*slots, std::memory_order_release);
+  return cudaSuccess;
+}
+
+template <typename K, typename... More>
+cudaError_t launch_chains(K kernel, size_t smem, const LinrecArgs& p, const Chains& chains,
+                          KernelSlots* known, int vec, int* cluster, cudaStream_t s,
+                          More... more) {
+  int slots = 0;
+  cudaError_t e = kernel_slots(kernel, smem, known, &slots);
+  if (e != cudaSuccess) return e;
   Chains ch = chains;
   const long long n = (long long)p.B * ch.nblk;
-  ch.cs = cluster_size(p, n, sms * (per > 0 ? per : 1));
+  ch.cs = cluster_size(p, n, slots);
   *cluster = ch.cs;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
