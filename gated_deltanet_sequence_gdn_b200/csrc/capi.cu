@@ -659,7 +659,7 @@ static int validate_rope(const QkRopeArgs& p, int more_flags) {
   if (!ok_opt_f32(p.q_weight) || !ok_opt_f32(p.k_weight) || !ok_opt_f32(p.dqw) ||
       !ok_opt_f32(p.dkw))
     return GDN_ERR_INVALID_ARG;
-  if (p.d > 256 || p.Hq + (long long)p.Hk > (1 << 20) || p.tokens > 0x7fffffffLL)
+  if (p.d > 256 || p.Hq + (long long)p.Hk > (1 << 20) || p.tokens > 0x3fffffffLL)
     return GDN_ERR_UNSUPPORTED;
   if (p.tokens == 0 || p.Hq + p.Hk == 0) return GDN_OK;
   const size_t es = elem_size(p.dtype);
