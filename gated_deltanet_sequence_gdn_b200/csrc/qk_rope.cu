@@ -85,7 +85,7 @@ struct FwdRun {
 template <typename T>
 cudaError_t run_fwd(const QkRopeArgs& a, cudaStream_t s) {
   Sides p = sides_of(a);
-  plan_warps(&p, sizeof(T) == 2 ? 4 : 2);
+  plan_warps(&p, sizeof(T) == 2 ? 4 : 2, 2);
   return by_size(p, vec_ok(p, sizeof(T), sizeof(T)), FwdRun<T>{p, s});
 }
 

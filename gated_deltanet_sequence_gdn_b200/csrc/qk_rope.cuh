@@ -287,14 +287,14 @@ inline bool rows16(const void* p, long long ld, int es) {
 }
 inline int group_of(int d) { return d <= 64 ? 8 : d <= 128 ? 16 : 32; }
 
-// How warps share a token: as many as leave each two rounds of the u heads that it brings in
+// How warps share a token: as many as leave each `rounds` of the u heads that it brings in
 // at once, so that what a warp does once a token (its angles) stays small beside its heads; q
 // and k get them as they have heads.
-inline void plan_warps(Sides* p, int u) {
+inline void plan_warps(Sides* p, int u, int rounds) {
   Side &q = p->s[0], &k = p->s[1];
   const int step = 32 / group_of(p->d) * u, H = q.H + k.H;
   int w = q.H > 0 && k.H > 0 ? 2 : 1;
-  while (w < kWarps && w * step * 2 < H) w *= 2;
+  while (w < kWarps && w * step * rounds < H) w *= 2;
   k.warps = k.H == 0 ? 0 : (int)((2LL * w * k.H + H) / (2 * H));
   if (k.H > 0 && k.warps == 0) k.warps = 1;
   if (q.H > 0 && k.warps == w) k.warps = w - 1;

@@ -143,7 +143,7 @@ qk_rope_sums_kernel(const float* partial, int blocks, int d, float* dqw, float* 
 // gradients): two a multiprocessor.
 constexpr int kBwdBlocks = 148 * 2;
 void plan_bwd(Sides* p) {
-  plan_warps(p, 2);
+  plan_warps(p, 2, 4);
   if (p->blocks > kBwdBlocks) p->blocks = kBwdBlocks;
 }
 template <typename T, typename TG>
