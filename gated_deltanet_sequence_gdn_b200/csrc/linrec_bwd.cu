@@ -17,9 +17,11 @@ struct BwdStage {
   alignas(128) TG b[kTileT * kTileC];
   alignas(128) TD dh[kTileT * kTileC];
 };
+// Two stages where they leave room for two blocks on a multiprocessor, else one.
 template <typename TX, typename TG, typename TD>
 struct BwdSmem {
-  BwdStage<TX, TG, TD> stage[2];
+  static constexpr int kStages = sizeof(BwdStage<TX, TG, TD>) <= 48 * 1024 ? 2 : 1;
+  BwdStage<TX, TG, TD> stage[kStages];
   CarrySmem carry;
   float2 back[kWarps][32];  // R of each warp's tokens: c_out = A c_in + R
   float4 sums[kWarps][32];
@@ -33,11 +35,12 @@ __device__ __forceinline__ void add_kept(float2* sum, float2* err, float2 v) {
 }
 
 template <typename TX, typename TG, bool GIVEN, int SCALE, typename TD, typename TDG>
-__global__ void __launch_bounds__(kLinrecThreads, sizeof(TX) + sizeof(TG) + sizeof(TD) == 6 ? 2 : 1)
+__global__ void __launch_bounds__(kLinrecThreads, 2)
 linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ LinrecMaps maps,
                   const float* states, float2* sums) {
   extern __shared__ __align__(128) unsigned char smem_raw[];
   using Smem = BwdSmem<TX, TG, TD>;
+  constexpr int kStages = Smem::kStages;
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
   FoldRow* folds = reinterpret_cast<FoldRow*>(smem_raw + sizeof(Smem));
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, first = warp * kPer;
@@ -53,10 +56,10 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
   };
   auto load = [&](int round) {
     const int n = length(round), t = tile(round) * kTileT;
-    BwdStage<TX, TG, TD>& st = sm.stage[round & 1];
+    BwdStage<TX, TG, TD>& st = sm.stage[round % kStages];
     if (ch.tma) {
       if (n > 0 && threadIdx.x == 0) {
-        uint64_t* bar = &sm.carry.loaded[round & 1];
+        uint64_t* bar = &sm.carry.loaded[round % kStages];
         const int y = ch.tab.cu ? (int)k.tok + t : t, z = ch.tab.cu ? 0 : k.row;
         tc::mbar_arrive_expect_tx(bar, sizeof(st.x) + sizeof(st.a) + (p.b ? sizeof(st.b) : 0) +
                                            sizeof(st.dh));
@@ -81,6 +84,8 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
   if (!GIVEN) gc = gate_const(p.A_log, p.dt_bias, c, p.D);
   float2 carry = read2(p.dht, k.row, c, p.D);  // behind the round's last tile (warp 0's)
   bool lost = false;
+  float2 hnext = both(0.f);
+  if (warp == 1 && last >= 0) hnext = read2(states, k.chunk0 + last, c, p.D);
   float2 sA = both(0.f), eA = both(0.f), sb = both(0.f), eb = both(0.f);
   Rows<TD> odx;
   Rows<TDG> oda, odb;
@@ -92,72 +97,77 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
     const int tt = tile(round), n = length(round);
     if (!ch.tma) {
       cp_async_wait<0>();
-    } else if (n > 0 && !tc::mbar_wait(&sm.carry.loaded[round & 1], (round >> 1) & 1, nullptr, 0)) {
+    } else if (n > 0 && !tc::mbar_wait(&sm.carry.loaded[round % kStages], (round / kStages) & 1,
+                                       nullptr, 0)) {
       report_timeout(ch.status, 0x4c54);
     }
     __syncthreads();  // the stage is complete, the other one free
-    if (round + 1 < rounds) load(round + 1);
-    BwdStage<TX, TG, TD>& st = sm.stage[round & 1];
+    if (kStages > 1 && round + 1 < rounds) load(round + 1);
+    float2 hs = hnext;  // warp 1's: the state before the tile
+    if (warp == 1 && tt - ch.cs >= 0) hnext = read2(states, k.chunk0 + tt - ch.cs, c, p.D);
+    BwdStage<TX, TG, TD>& st = sm.stage[round % kStages];
     if (n > 0 && n < kTileT && ch.tab.cu) {  // the next sequence's tokens
       clear_rows(st.x, n);
       tc::fence_proxy_async_smem();  // the stage's next tiles come by TMA
       __syncthreads();
     }
     const int mine = first * kTileC + 2 * lane;
-    float2 al[kPer], be[kPer], f[kPer];
-    float2 A = both(1.f), H = both(0.f), R = both(0.f);
+    float2 e[kPer], slope[kPer], be[kPer];
+    {
+      float2 al[kPer], A = both(1.f), H = both(0.f), R = both(0.f);
 #pragma unroll
-    for (int i0 = 0; i0 < kPer; i0 += kGroup) {
-      float2 e[kGroup];
+      for (int i0 = 0; i0 < kPer; i0 += kGroup) {
 #pragma unroll
-      for (int i = 0; i < kGroup; ++i) e[i] = get2(st.a + mine + (i0 + i) * kTileC);
-      decay_exponents<GIVEN, kGroup>(e, gc);
-#pragma unroll
-      for (int i = 0; i < kGroup; ++i) {
-        al[i0 + i] = ex2_2(e[i]);
-        be[i0 + i] = p.b ? get2(st.b + mine + (i0 + i) * kTileC) : both(1.f);
-      }
-      input_scales<SCALE, kGroup>(e, al + i0, f + i0);
-      if (p.b) write_gates<GIVEN, kGroup>(be + i0);
-    }
-    if (n < kTileT) {  // behind the sequence: both states pass through
-#pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (first + i >= n) {
-          al[i] = both(1.f);
-          be[i] = both(0.f);
+        for (int i = 0; i < kGroup; ++i) {
+          e[i0 + i] = get2(st.a + mine + (i0 + i) * kTileC);
+          be[i0 + i] = p.b ? get2(st.b + mine + (i0 + i) * kTileC) : both(1.f);
         }
-    }
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      float2 u = mul2(get2(st.x + mine + i * kTileC), be[i]);
-      if (SCALE != kScaleNone) u = mul2(u, f[i]);
-      H = fma2(al[i], H, u);
-      A = mul2(A, al[i]);
-    }
-#pragma unroll
-    for (int i = kPer - 1; i >= 0; --i) {
-      if (first + i < n) R = add2(get2(st.dh + mine + i * kTileC), R);
-      R = mul2(al[i], R);
-    }
-    sm.carry.fold[warp][lane] = join4(A, H);
-    sm.back[warp][lane] = R;
-    __syncthreads();
-    if (warp == 0) {
-      float2 hs = n > 0 ? read2(states, k.chunk0 + tt, c, p.D) : both(0.f);
-      A = both(1.f);
-      R = both(0.f);
-#pragma unroll 4
-      for (int w = kWarps - 1; w >= 0; --w) {
-        const float2 a = first2(sm.carry.fold[w][lane]);
-        R = fma2(a, R, sm.back[w][lane]);
-        A = mul2(A, a);
+        if (GIVEN) decay_exponents<true, kGroup>(e + i0, gc);
+        else decay_exponents_slope<kGroup>(e + i0, gc, slope + i0);
+        if (p.b) write_gates<GIVEN, kGroup>(be + i0);
       }
+      if (n < kTileT) {  // behind the sequence: both states pass through
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          if (first + i >= n) e[i] = be[i] = both(0.f);
+      }
+#pragma unroll
+      for (int i0 = 0; i0 < kPer; i0 += kGroup) {
+        float2 f[kGroup];
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) al[i0 + i] = ex2_2(e[i0 + i]);
+        if (SCALE != kScaleNone) input_scales<SCALE, kGroup>(e + i0, al + i0, f);
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) {
+          float2 u = mul2(get2(st.x + mine + (i0 + i) * kTileC), be[i0 + i]);
+          if (SCALE != kScaleNone) u = mul2(u, f[i]);
+          H = fma2(al[i0 + i], H, u);
+          A = mul2(A, al[i0 + i]);
+        }
+      }
+#pragma unroll
+      for (int i = kPer - 1; i >= 0; --i) {
+        if (first + i < n) R = add2(get2(st.dh + mine + i * kTileC), R);
+        R = mul2(al[i], R);
+      }
+      sm.carry.fold[warp][lane] = join4(A, H);
+      sm.back[warp][lane] = R;
+    }
+    __syncthreads();
+    if (warp == 1) {  // the state through the tile
 #pragma unroll 4
       for (int w = 0; w < kWarps; ++w) {
         sm.carry.start[w][lane] = hs;
         const float4 q = sm.carry.fold[w][lane];
         hs = fma2(first2(q), hs, last2(q));
+      }
+    } else if (warp == 0) {  // its gradient
+      float2 A = both(1.f), R = both(0.f);
+#pragma unroll 4
+      for (int w = kWarps - 1; w >= 0; --w) {
+        const float2 a = first2(sm.carry.fold[w][lane]);
+        R = fma2(a, R, sm.back[w][lane]);
+        A = mul2(A, a);
       }
       float2 v = carry_round(ch, k.rank, round, join4(A, R), sm.carry, folds, &carry, &lost);
 #pragma unroll 4
@@ -168,7 +178,15 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
       }
     }
     __syncthreads();
-    float2 hs = sm.carry.start[warp][lane];
+    hs = sm.carry.start[warp][lane];
+    float2 al[kPer], f[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) al[i] = ex2_2(e[i]);
+    if (SCALE != kScaleNone) {
+#pragma unroll
+      for (int i0 = 0; i0 < kPer; i0 += kGroup)
+        input_scales<SCALE, kGroup>(e + i0, al + i0, f + i0);
+    }
     float2 hp[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -181,51 +199,39 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
     float2 tA = both(0.f), tb = both(0.f);
     const bool whole = n == kTileT && cols > 1 && vec;
 #pragma unroll
-    for (int i0 = kPer - kGroup; i0 >= 0; i0 -= kGroup) {
-      float2 e[kGroup], slope[kGroup];
-      if (!GIVEN) {
-#pragma unroll
-        for (int i = 0; i < kGroup; ++i) e[i] = get2(st.a + mine + (i0 + i) * kTileC);
-        decay_exponents_slope<kGroup>(e, gc, slope);
+    for (int i = kPer - 1; i >= 0; --i) {
+      if (first + i >= n) continue;
+      const int at = mine + i * kTileC;
+      const float2 lam = add2(get2(st.dh + at), cc);
+      cc = mul2(al[i], lam);
+      const float2 lx = mul2(lam, get2(st.x + at));
+      float2 dg = mul2(cc, hp[i]), dx = mul2(lam, be[i]), db = lx;
+      if (SCALE != kScaleNone) {
+        const float2 q = make_float2(input_scale_slope<SCALE>(al[i].x, f[i].x),
+                                     input_scale_slope<SCALE>(al[i].y, f[i].y));
+        dg = fma2(mul2(lx, be[i]), q, dg);
+        dx = mul2(dx, f[i]);
+        db = mul2(db, f[i]);
       }
-#pragma unroll
-      for (int j = kGroup - 1; j >= 0; --j) {
-        const int i = i0 + j, at = mine + i * kTileC;
-        if (first + i >= n) continue;
-        const float2 lam = add2(get2(st.dh + at), cc);
-        cc = mul2(al[i], lam);
-        const float2 lx = mul2(lam, get2(st.x + at));
-        float2 dg = mul2(cc, hp[i]);
-        if (SCALE != kScaleNone) {
-          const float2 q = make_float2(input_scale_slope<SCALE>(al[i].x, f[i].x),
-                                       input_scale_slope<SCALE>(al[i].y, f[i].y));
-          dg = fma2(mul2(lx, be[i]), q, dg);
-        }
-        float2 dx = mul2(lam, be[i]), db = lx, da = dg;
-        if (SCALE != kScaleNone) {
-          dx = mul2(dx, f[i]);
-          db = mul2(db, f[i]);
-        }
-        if (!GIVEN) {
-          if (p.b) db = mul2(mul2(db, be[i]), write_gate_rest(get2(st.b + at), be[i]));
-          da = mul2(dg, slope[j]);
-          tb = add2(tb, da);
-          // dg log2(e) times e; e = -inf where alpha = 0
-          tA = add2(tA, make_float2(dg.x == 0.f ? 0.f : dg.x * e[j].x,
-                                    dg.y == 0.f ? 0.f : dg.y * e[j].y));
-        }
-        TD* px = odx.at(i);
-        TDG* pa = oda.at(i);
-        TDG* pb = odb.at(i);
-        if (whole) {
-          put2(px, dx);
-          put2(pa, da);
-          if (p.b) put2(pb, db);
-        } else {
-          put2(px, dx, cols);
-          put2(pa, da, cols);
-          if (p.b) put2(pb, db, cols);
-        }
+      float2 da = dg;
+      if (!GIVEN) {
+        if (p.b) db = mul2(mul2(db, be[i]), write_gate_rest(get2(st.b + at), be[i]));
+        da = mul2(dg, slope[i]);
+        tb = add2(tb, da);
+        // dg log2(e) times e, which is -inf where alpha = 0
+        tA = fma2(dg, make_float2(fmaxf(e[i].x, -3e38f), fmaxf(e[i].y, -3e38f)), tA);
+      }
+      TD* px = odx.at(i);
+      TDG* pa = oda.at(i);
+      TDG* pb = odb.at(i);
+      if (whole) {
+        put2(px, dx);
+        put2(pa, da);
+        if (p.b) put2(pb, db);
+      } else {
+        put2(px, dx, cols);
+        put2(pa, da, cols);
+        if (p.b) put2(pb, db, cols);
       }
     }
     odx.advance(-step);
@@ -234,6 +240,10 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
     if (!GIVEN) {  // a lane keeps its channels: their sums run through the rounds
       add_kept(&sA, &eA, tA);
       add_kept(&sb, &eb, tb);
+    }
+    if (kStages == 1 && round + 1 < rounds) {
+      __syncthreads();  // the stage is read
+      load(round + 1);
     }
   }
   if (k.rank == 0 && warp == 0) write2(p.dh0, k.row, c, p.D, carry);

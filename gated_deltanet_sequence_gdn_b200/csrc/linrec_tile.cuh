@@ -182,15 +182,19 @@ __device__ __forceinline__ void cp_async_wait() {
 template <typename T>
 __device__ __forceinline__ void load_elements(T* dst, const void* base, long long ld,
                                               long long tok, int n, int c0, int D) {
-  const T* src = static_cast<const T*>(base) + tok * ld + c0;
-#pragma unroll 4
-  for (int i = 0; i < kTileT * kTileC / kLinrecThreads; ++i) {
-    const int k = threadIdx.x + i * kLinrecThreads, r = k / kTileC, c = k % kTileC;
-    const bool in = r < n && c < D - c0;
+  constexpr int kStep = kLinrecThreads / kTileC;  // rows at once
+  const int r0 = threadIdx.x / kTileC, c = threadIdx.x % kTileC;
+  const bool in = c < D - c0;
+  const T* src = static_cast<const T*>(base) + (tok + r0) * ld + c0 + (in ? c : 0);
+  dst += threadIdx.x;
+#pragma unroll 8
+  for (int r = 0; r < kTileT; r += kStep) {
+    const bool here = in && r0 + r < n;
     if (sizeof(T) == 4)
-      cp_async4(dst + k, in ? src + r * ld + c : src, in ? 4 : 0);
+      cp_async4(dst + r * kTileC, here ? static_cast<const void*>(src) : base, here ? 4 : 0);
     else
-      dst[k] = in ? src[r * ld + c] : from_f32<T>(0.f);
+      dst[r * kTileC] = here ? *src : from_f32<T>(0.f);
+    src += kStep * ld;
   }
 }
 // Clears the rows of a tile behind its n tokens.
