@@ -17,9 +17,9 @@ namespace {
 
 template <typename TX, typename TG>
 struct FwdStage {
-  alignas(128) TX x[kTileT * kTileC];
-  alignas(128) TG a[kTileT * kTileC];
-  alignas(128) TG b[kTileT * kTileC];
+  alignas(128) TX x[kTile];
+  alignas(128) TG a[kTile];
+  alignas(128) TG b[kTile];
 };
 template <typename TX, typename TG>
 struct FwdSmem {
@@ -27,15 +27,16 @@ struct FwdSmem {
   CarrySmem carry;
 };
 
-template <typename TX, typename TG, bool GIVEN, int SCALE, typename TO>
+template <typename TX, typename TG, bool GIVEN, int SCALE, typename TO, bool NARROW>
 __global__ void __launch_bounds__(kLinrecThreads, sizeof(TX) + sizeof(TG) == 4 ? 4 : 2)
 linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ LinrecMaps maps) {
   extern __shared__ __align__(128) unsigned char smem_raw[];
   auto& sm = *reinterpret_cast<FwdSmem<TX, TG>*>(smem_raw);
   FoldRow* folds = reinterpret_cast<FoldRow*>(smem_raw + sizeof(FwdSmem<TX, TG>));
-  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-  const Chain k = chain_of(p, ch);
-  const int c = k.c0 + 2 * lane, cols = p.D - c;
+  constexpr int kTileT = Shape<NARROW>::kT, kC = Shape<NARROW>::kC, kTileChunks = kTileT / kLinrecChunk;
+  const Spot<NARROW> at;
+  const Chain k = chain_of<NARROW>(p, ch);
+  const int c = k.c0 + 2 * at.cl, cols = p.D - c;
   const int step = ch.cs * kTileT;
   const int tokens = (int)k.len - k.rank * kTileT;  // from the block's first tile on
   auto length = [&](int round) {
@@ -56,9 +57,9 @@ linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
       }
     } else {
       if (n > 0) {
-        load_elements(st.x, p.x, p.ldx, k.tok + t, n, k.c0, p.D);
-        load_elements(st.a, p.a, p.lda, k.tok + t, n, k.c0, p.D);
-        if (p.b) load_elements(st.b, p.b, p.ldb, k.tok + t, n, k.c0, p.D);
+        load_elements<NARROW>(st.x, p.x, p.ldx, k.tok + t, n, k.c0, p.D);
+        load_elements<NARROW>(st.a, p.a, p.lda, k.tok + t, n, k.c0, p.D);
+        if (p.b) load_elements<NARROW>(st.b, p.b, p.ldb, k.tok + t, n, k.c0, p.D);
       }
       cp_async_commit();
     }
@@ -70,8 +71,8 @@ linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
   float2 carry = read2(p.h0, k.row, c, p.D);  // before the round's first tile (warp 0's)
   bool lost = false;
   Rows<TO> out;
-  out.begin(p.h, p.ldh, k.tok + k.rank * kTileT, k.c0, warp * kPer, 2 * lane);
-  const int rounds = (k.chunks + ch.cs - 1) / ch.cs;
+  out.begin(p.h, p.ldh, k.tok + k.rank * kTileT, k.c0, at.first, 2 * at.cl);
+  const int rounds = (k.tiles + ch.cs - 1) / ch.cs;
   for (int round = 0; round < rounds; ++round) {
     const int n = length(round);
     if (!ch.tma) {
@@ -82,18 +83,18 @@ linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
     __syncthreads();  // the stage is complete, the other one free
     if (round + 1 < rounds) load(round + 1);
     const FwdStage<TX, TG>& st = sm.stage[round & 1];
-    const int mine = warp * kPer * kTileC + 2 * lane;
+    const int mine = at.mine();
     float2 al[kPer], u[kPer];
 #pragma unroll
     for (int i0 = 0; i0 < kPer; i0 += kGroup) {
       float2 e[kGroup];
 #pragma unroll
-      for (int i = 0; i < kGroup; ++i) e[i] = get2(st.a + mine + (i0 + i) * kTileC);
+      for (int i = 0; i < kGroup; ++i) e[i] = get2(st.a + mine + (i0 + i) * kC);
       decay_exponents<GIVEN, kGroup>(e, gc);
 #pragma unroll
       for (int i = 0; i < kGroup; ++i) {
         al[i0 + i] = ex2_2(e[i]);
-        u[i0 + i] = get2(st.x + mine + (i0 + i) * kTileC);
+        u[i0 + i] = get2(st.x + mine + (i0 + i) * kC);
       }
       if (SCALE != kScaleNone) {
         float2 f[kGroup];
@@ -104,7 +105,7 @@ linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
       if (p.b) {
         float2 b[kGroup];
 #pragma unroll
-        for (int i = 0; i < kGroup; ++i) b[i] = get2(st.b + mine + (i0 + i) * kTileC);
+        for (int i = 0; i < kGroup; ++i) b[i] = get2(st.b + mine + (i0 + i) * kC);
         write_gates<GIVEN, kGroup>(b);
 #pragma unroll
         for (int i = 0; i < kGroup; ++i) u[i0 + i] = mul2(u[i0 + i], b[i]);
@@ -113,7 +114,7 @@ linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
     if (n < kTileT) {  // behind the sequence: the state passes through
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        if (warp * kPer + i >= n) {
+        if (at.first + i >= n) {
           al[i] = both(1.f);
           u[i] = both(0.f);
         }
@@ -124,29 +125,32 @@ linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
       H = fma2(al[i], H, u[i]);
       A = mul2(A, al[i]);
     }
-    sm.carry.fold[warp][lane] = join4(A, H);
+    sm.carry.fold[threadIdx.x] = join4(A, H);
     __syncthreads();
-    if (warp == 0) {
+    if (at.warp == 0) {
       A = both(1.f);
       H = both(0.f);
 #pragma unroll 4
-      for (int w = 0; w < kWarps; ++w) {
-        const float4 f = sm.carry.fold[w][lane];
+      for (int w = 0; w < 8; ++w) {
+        const float4 f = sm.carry.fold[at.group(w)];
         H = fma2(first2(f), H, last2(f));
         A = mul2(A, first2(f));
       }
-      float2 v = carry_round(ch, k.rank, round, join4(A, H), sm.carry, folds, &carry, &lost);
-      if (n > 0) write2(p.states_out, k.chunk0 + round * ch.cs + k.rank, c, p.D, v);
+      float2 v = carry_round<NARROW, false>(ch, k.rank, round, join4(A, H), sm.carry, folds, &carry,
+                                            &lost);
+      if (n > at.half * kLinrecChunk)
+        write2(p.states_out,
+               k.chunk0 + (long long)(round * ch.cs + k.rank) * kTileChunks + at.half, c, p.D, v);
 #pragma unroll 4
-      for (int w = 0; w < kWarps; ++w) {
-        sm.carry.start[w][lane] = v;
-        const float4 f = sm.carry.fold[w][lane];
+      for (int w = 0; w < 8; ++w) {
+        sm.carry.start[at.group(w)] = v;
+        const float4 f = sm.carry.fold[at.group(w)];
         v = fma2(first2(f), v, last2(f));
       }
     }
     __syncthreads();
     if (p.h) {
-      float2 h = sm.carry.start[warp][lane];
+      float2 h = sm.carry.start[threadIdx.x];
       if (n == kTileT && cols > 1 && vec) {
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
@@ -157,13 +161,13 @@ linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           h = fma2(al[i], h, u[i]);
-          if (warp * kPer + i < n) put2(out.at(i), h, cols);
+          if (at.first + i < n) put2(out.at(i), h, cols);
         }
       }
       out.advance(step);
     }
   }
-  if (k.rank == 0 && warp == 0) write2(p.ht, k.row, c, p.D, carry);
+  if (k.rank == 0 && at.warp == 0 && at.half == 0) write2(p.ht, k.row, c, p.D, carry);
   carry_end(ch);
 }
 
@@ -235,18 +239,29 @@ cudaError_t fill_seq_table(const long long* cu, int B, const SeqTab& tab, cudaSt
 struct FwdRun {
   const LinrecArgs& p;
   const Chains& ch;
+  int vec;  // the rows of h take pairs
   cudaStream_t s;
   template <typename TX, typename TG, bool GIVEN, int SCALE, bool WIDE>
   cudaError_t run() const {
     using TO = typename Wide<TX, WIDE>::type;
+    static KernelSlots known, known_narrow;
+    const auto kernel = linrec_fwd_kernel<TX, TG, GIVEN, SCALE, TO, false>;
+    int slots = 0, cs = 1;
+    cudaError_t e = kernel_slots(kernel, sizeof(FwdSmem<TX, TG>), &known, &slots);
+    if (e != cudaSuccess) return e;
+    return narrow_tiles(p, slots)
+               ? launch<TX, TG, true>(linrec_fwd_kernel<TX, TG, GIVEN, SCALE, TO, true>,
+                                      &known_narrow, &cs)
+               : launch<TX, TG, false>(kernel, &known, &cs);
+  }
+  template <typename TX, typename TG, bool NARROW, typename K>
+  cudaError_t launch(K kernel, KernelSlots* known, int* cs) const {
     LinrecMaps maps;
     Chains c = ch;
-    c.tma = map_tiles<TX>(&maps.x, p, p.x, p.ldx) && map_tiles<TG>(&maps.a, p, p.a, p.lda) &&
-            (!p.b || map_tiles<TG>(&maps.b, p, p.b, p.ldb));
-    static KernelSlots known;
-    int cs = 1;
-    return launch_chains(linrec_fwd_kernel<TX, TG, GIVEN, SCALE, TO>, sizeof(FwdSmem<TX, TG>), p,
-                         c, &known, pairs(p.h, p.ldh, sizeof(TO)), &cs, s, maps);
+    c.tma = map_tiles<NARROW, TX>(&maps.x, p, p.x, p.ldx) &&
+            map_tiles<NARROW, TG>(&maps.a, p, p.a, p.lda) &&
+            (!p.b || map_tiles<NARROW, TG>(&maps.b, p, p.b, p.ldb));
+    return launch_chains<NARROW>(kernel, sizeof(FwdSmem<TX, TG>), p, c, known, vec, cs, s, maps);
   }
 };
 struct StepRun {
@@ -271,7 +286,6 @@ size_t linrec_workspace_bytes(const long long* cu, int B, int T, int D) {
 
 cudaError_t make_chains(const LinrecArgs& a, void* workspace, bool table, cudaStream_t s,
                         Chains* ch) {
-  ch->nblk = (a.D + kTileC - 1) / kTileC;
   if (a.cu) {
     char* ws = static_cast<char*>(workspace);
     ch->tab.cu = reinterpret_cast<const long long*>(ws);
@@ -292,7 +306,8 @@ cudaError_t make_chains(const LinrecArgs& a, void* workspace, bool table, cudaSt
 
 cudaError_t launch_linrec_scan(const LinrecArgs& a, const Chains& ch, int wide_flag,
                                cudaStream_t s) {
-  return by_type(a, wide_flag, FwdRun{a, ch, s});
+  const int wide = a.dtype == GDN_F32 || (a.flags & wide_flag);
+  return by_type(a, wide_flag, FwdRun{a, ch, pairs(a.h, a.ldh, wide ? 4 : 2), s});
 }
 
 cudaError_t launch_linrec_fwd(const LinrecArgs& a, void* workspace, cudaStream_t s) {

@@ -12,10 +12,10 @@ namespace {
 
 template <typename TX, typename TG, typename TD>
 struct BwdStage {
-  alignas(128) TX x[kTileT * kTileC];
-  alignas(128) TG a[kTileT * kTileC];
-  alignas(128) TG b[kTileT * kTileC];
-  alignas(128) TD dh[kTileT * kTileC];
+  alignas(128) TX x[kTile];
+  alignas(128) TG a[kTile];
+  alignas(128) TG b[kTile];
+  alignas(128) TD dh[kTile];
 };
 // Two stages where they leave room for two blocks on a multiprocessor, else one.
 template <typename TX, typename TG, typename TD>
@@ -23,8 +23,8 @@ struct BwdSmem {
   static constexpr int kStages = sizeof(BwdStage<TX, TG, TD>) <= 48 * 1024 ? 2 : 1;
   BwdStage<TX, TG, TD> stage[kStages];
   CarrySmem carry;
-  float2 back[kWarps][32];  // R of each warp's tokens: c_out = A c_in + R
-  float4 sums[kWarps][32];
+  float2 back[kLinrecThreads];  // R of each thread's tokens: c_out = A c_in + R
+  float4 sums[kLinrecThreads];
 };
 
 // sum += v with the rounding error kept in err.
@@ -34,7 +34,7 @@ __device__ __forceinline__ void add_kept(float2* sum, float2* err, float2 v) {
   *sum = t;
 }
 
-template <typename TX, typename TG, bool GIVEN, int SCALE, typename TD, typename TDG>
+template <typename TX, typename TG, bool GIVEN, int SCALE, typename TD, typename TDG, bool NARROW>
 __global__ void __launch_bounds__(kLinrecThreads, 2)
 linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ LinrecMaps maps,
                   const float* states, float2* sums) {
@@ -43,11 +43,13 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
   constexpr int kStages = Smem::kStages;
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
   FoldRow* folds = reinterpret_cast<FoldRow*>(smem_raw + sizeof(Smem));
-  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, first = warp * kPer;
-  const Chain k = chain_of(p, ch);
-  const int c = k.c0 + 2 * lane, cols = p.D - c;
+  constexpr int kTileT = Shape<NARROW>::kT, kC = Shape<NARROW>::kC, kTileChunks = kTileT / kLinrecChunk;
+  const Spot<NARROW> at;
+  const int first = at.first;
+  const Chain k = chain_of<NARROW>(p, ch);
+  const int c = k.c0 + 2 * at.cl, cols = p.D - c;
   const int step = ch.cs * kTileT;
-  const int last = k.chunks - 1 - k.rank;  // the block's first tile; may be before the sequence
+  const int last = k.tiles - 1 - k.rank;  // the block's first tile; may be before the sequence
   const long long tok0 = k.tok + last * (long long)kTileT;
   const int tokens = (int)k.len - last * kTileT;  // from there to the sequence's end
   auto tile = [&](int round) { return last - round * ch.cs; };
@@ -70,10 +72,10 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
       }
     } else {
       if (n > 0) {
-        load_elements(st.x, p.x, p.ldx, k.tok + t, n, k.c0, p.D);
-        load_elements(st.a, p.a, p.lda, k.tok + t, n, k.c0, p.D);
-        if (p.b) load_elements(st.b, p.b, p.ldb, k.tok + t, n, k.c0, p.D);
-        load_elements(st.dh, p.dh, p.lddh, k.tok + t, n, k.c0, p.D);
+        load_elements<NARROW>(st.x, p.x, p.ldx, k.tok + t, n, k.c0, p.D);
+        load_elements<NARROW>(st.a, p.a, p.lda, k.tok + t, n, k.c0, p.D);
+        if (p.b) load_elements<NARROW>(st.b, p.b, p.ldb, k.tok + t, n, k.c0, p.D);
+        load_elements<NARROW>(st.dh, p.dh, p.lddh, k.tok + t, n, k.c0, p.D);
       }
       cp_async_commit();
     }
@@ -84,15 +86,19 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
   if (!GIVEN) gc = gate_const(p.A_log, p.dt_bias, c, p.D);
   float2 carry = read2(p.dht, k.row, c, p.D);  // behind the round's last tile (warp 0's)
   bool lost = false;
+  auto state = [&](int tt) {  // before the lane's chunk of a tile
+    const int j = tt * kTileChunks + at.half;
+    return tt >= 0 && j < k.chunks ? read2(states, k.chunk0 + j, c, p.D) : both(0.f);
+  };
   float2 hnext = both(0.f);
-  if (warp == 1 && last >= 0) hnext = read2(states, k.chunk0 + last, c, p.D);
+  if (at.warp == 1) hnext = state(last);
   float2 sA = both(0.f), eA = both(0.f), sb = both(0.f), eb = both(0.f);
   Rows<TD> odx;
   Rows<TDG> oda, odb;
-  odx.begin(p.dx, p.lddx, tok0, k.c0, first, 2 * lane);
-  oda.begin(p.da, p.ldda, tok0, k.c0, first, 2 * lane);
-  odb.begin(p.db, p.lddb, tok0, k.c0, first, 2 * lane);
-  const int rounds = (k.chunks + ch.cs - 1) / ch.cs;
+  odx.begin(p.dx, p.lddx, tok0, k.c0, first, 2 * at.cl);
+  oda.begin(p.da, p.ldda, tok0, k.c0, first, 2 * at.cl);
+  odb.begin(p.db, p.lddb, tok0, k.c0, first, 2 * at.cl);
+  const int rounds = (k.tiles + ch.cs - 1) / ch.cs;
   for (int round = 0; round < rounds; ++round) {
     const int tt = tile(round), n = length(round);
     if (!ch.tma) {
@@ -103,15 +109,15 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
     }
     __syncthreads();  // the stage is complete, the other one free
     if (kStages > 1 && round + 1 < rounds) load(round + 1);
-    float2 hs = hnext;  // warp 1's: the state before the tile
-    if (warp == 1 && tt - ch.cs >= 0) hnext = read2(states, k.chunk0 + tt - ch.cs, c, p.D);
+    float2 hs = hnext;  // warp 1's
+    if (at.warp == 1) hnext = state(tt - ch.cs);
     BwdStage<TX, TG, TD>& st = sm.stage[round % kStages];
     if (n > 0 && n < kTileT && ch.tab.cu) {  // the next sequence's tokens
-      clear_rows(st.x, n);
+      clear_rows<NARROW>(st.x, n);
       tc::fence_proxy_async_smem();  // the stage's next tiles come by TMA
       __syncthreads();
     }
-    const int mine = first * kTileC + 2 * lane;
+    const int mine = at.mine();
     float2 e[kPer], slope[kPer], be[kPer];
     {
       float2 al[kPer], A = both(1.f), H = both(0.f), R = both(0.f);
@@ -119,8 +125,8 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
       for (int i0 = 0; i0 < kPer; i0 += kGroup) {
 #pragma unroll
         for (int i = 0; i < kGroup; ++i) {
-          e[i0 + i] = get2(st.a + mine + (i0 + i) * kTileC);
-          be[i0 + i] = p.b ? get2(st.b + mine + (i0 + i) * kTileC) : both(1.f);
+          e[i0 + i] = get2(st.a + mine + (i0 + i) * kC);
+          be[i0 + i] = p.b ? get2(st.b + mine + (i0 + i) * kC) : both(1.f);
         }
         if (GIVEN) decay_exponents<true, kGroup>(e + i0, gc);
         else decay_exponents_slope<kGroup>(e + i0, gc, slope + i0);
@@ -139,7 +145,7 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
         if (SCALE != kScaleNone) input_scales<SCALE, kGroup>(e + i0, al + i0, f);
 #pragma unroll
         for (int i = 0; i < kGroup; ++i) {
-          float2 u = mul2(get2(st.x + mine + (i0 + i) * kTileC), be[i0 + i]);
+          float2 u = mul2(get2(st.x + mine + (i0 + i) * kC), be[i0 + i]);
           if (SCALE != kScaleNone) u = mul2(u, f[i]);
           H = fma2(al[i0 + i], H, u);
           A = mul2(A, al[i0 + i]);
@@ -147,38 +153,39 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
       }
 #pragma unroll
       for (int i = kPer - 1; i >= 0; --i) {
-        if (first + i < n) R = add2(get2(st.dh + mine + i * kTileC), R);
+        if (first + i < n) R = add2(get2(st.dh + mine + i * kC), R);
         R = mul2(al[i], R);
       }
-      sm.carry.fold[warp][lane] = join4(A, H);
-      sm.back[warp][lane] = R;
+      sm.carry.fold[threadIdx.x] = join4(A, H);
+      sm.back[threadIdx.x] = R;
     }
     __syncthreads();
-    if (warp == 1) {  // the state through the tile
+    if (at.warp == 1) {  // the state through the lane's chunk
 #pragma unroll 4
-      for (int w = 0; w < kWarps; ++w) {
-        sm.carry.start[w][lane] = hs;
-        const float4 q = sm.carry.fold[w][lane];
+      for (int w = 0; w < 8; ++w) {
+        sm.carry.start[at.group(w)] = hs;
+        const float4 q = sm.carry.fold[at.group(w)];
         hs = fma2(first2(q), hs, last2(q));
       }
-    } else if (warp == 0) {  // its gradient
+    } else if (at.warp == 0) {  // its gradient
       float2 A = both(1.f), R = both(0.f);
 #pragma unroll 4
-      for (int w = kWarps - 1; w >= 0; --w) {
-        const float2 a = first2(sm.carry.fold[w][lane]);
-        R = fma2(a, R, sm.back[w][lane]);
+      for (int w = 7; w >= 0; --w) {
+        const float2 a = first2(sm.carry.fold[at.group(w)]);
+        R = fma2(a, R, sm.back[at.group(w)]);
         A = mul2(A, a);
       }
-      float2 v = carry_round(ch, k.rank, round, join4(A, R), sm.carry, folds, &carry, &lost);
+      float2 v = carry_round<NARROW, true>(ch, k.rank, round, join4(A, R), sm.carry, folds, &carry,
+                                           &lost);
 #pragma unroll 4
-      for (int w = kWarps - 1; w >= 0; --w) {
-        const float2 r = sm.back[w][lane];
-        sm.back[w][lane] = v;
-        v = fma2(first2(sm.carry.fold[w][lane]), v, r);
+      for (int w = 7; w >= 0; --w) {
+        const float2 r = sm.back[at.group(w)];
+        sm.back[at.group(w)] = v;
+        v = fma2(first2(sm.carry.fold[at.group(w)]), v, r);
       }
     }
     __syncthreads();
-    hs = sm.carry.start[warp][lane];
+    hs = sm.carry.start[threadIdx.x];
     float2 al[kPer], f[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) al[i] = ex2_2(e[i]);
@@ -191,20 +198,20 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       hp[i] = hs;
-      float2 u = mul2(get2(st.x + mine + i * kTileC), be[i]);
+      float2 u = mul2(get2(st.x + mine + i * kC), be[i]);
       if (SCALE != kScaleNone) u = mul2(u, f[i]);
       hs = fma2(al[i], hs, u);
     }
-    float2 cc = sm.back[warp][lane];
+    float2 cc = sm.back[threadIdx.x];
     float2 tA = both(0.f), tb = both(0.f);
     const bool whole = n == kTileT && cols > 1 && vec;
 #pragma unroll
     for (int i = kPer - 1; i >= 0; --i) {
       if (first + i >= n) continue;
-      const int at = mine + i * kTileC;
-      const float2 lam = add2(get2(st.dh + at), cc);
+      const int el = mine + i * kC;
+      const float2 lam = add2(get2(st.dh + el), cc);
       cc = mul2(al[i], lam);
-      const float2 lx = mul2(lam, get2(st.x + at));
+      const float2 lx = mul2(lam, get2(st.x + el));
       float2 dg = mul2(cc, hp[i]), dx = mul2(lam, be[i]), db = lx;
       if (SCALE != kScaleNone) {
         const float2 q = make_float2(input_scale_slope<SCALE>(al[i].x, f[i].x),
@@ -215,7 +222,7 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
       }
       float2 da = dg;
       if (!GIVEN) {
-        if (p.b) db = mul2(mul2(db, be[i]), write_gate_rest(get2(st.b + at), be[i]));
+        if (p.b) db = mul2(mul2(db, be[i]), write_gate_rest(get2(st.b + el), be[i]));
         da = mul2(dg, slope[i]);
         tb = add2(tb, da);
         // dg log2(e) times e, which is -inf where alpha = 0
@@ -246,15 +253,14 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
       load(round + 1);
     }
   }
-  if (k.rank == 0 && warp == 0) write2(p.dh0, k.row, c, p.D, carry);
+  if (k.rank == 0 && at.warp == 0 && at.half == 0) write2(p.dh0, k.row, c, p.D, carry);
   if (!GIVEN) {
-    sm.sums[warp][lane] = join4(mul2(sA, both(kLn2)), sb);
+    sm.sums[threadIdx.x] = join4(mul2(sA, both(kLn2)), sb);
     __syncthreads();
-    if (warp == 0) {
+    if (at.warp == 0 && at.half == 0) {
       float2 vA = both(0.f), vb = both(0.f);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float4 q = sm.sums[w][lane];
+      for (int i = at.cl; i < kLinrecThreads; i += Shape<NARROW>::kLanes) {
+        const float4 q = sm.sums[i];
         vA = add2(vA, first2(q));
         vb = add2(vb, last2(q));
       }
@@ -307,19 +313,32 @@ struct BwdRun {
   cudaError_t run() const {
     using TD = typename Wide<TX, WIDE>::type;
     using TDG = typename Wide<TD, GIVEN>::type;
+    static KernelSlots known, known_narrow;
+    const auto kernel = linrec_bwd_kernel<TX, TG, GIVEN, SCALE, TD, TDG, false>;
+    int slots = 0;
+    cudaError_t e = kernel_slots(kernel, sizeof(BwdSmem<TX, TG, TD>), &known, &slots);
+    if (e != cudaSuccess) return e;
+    return narrow_tiles(p, slots)
+               ? launch<TX, TG, GIVEN, TD, TDG, true>(
+                     linrec_bwd_kernel<TX, TG, GIVEN, SCALE, TD, TDG, true>, &known_narrow)
+               : launch<TX, TG, GIVEN, TD, TDG, false>(kernel, &known);
+  }
+  template <typename TX, typename TG, bool GIVEN, typename TD, typename TDG, bool NARROW,
+            typename K>
+  cudaError_t launch(K kernel, KernelSlots* known) const {
     LinrecMaps maps;
     Chains c = ch;
-    c.tma = map_tiles<TX>(&maps.x, p, p.x, p.ldx) && map_tiles<TG>(&maps.a, p, p.a, p.lda) &&
-            (!p.b || map_tiles<TG>(&maps.b, p, p.b, p.ldb)) &&
-            map_tiles<TD>(&maps.dh, p, p.dh, p.lddh);
-    const bool alone = p.B == 1 && most_blocks(p) == 1;  // one block a channel: no sums to join
+    c.tma = map_tiles<NARROW, TX>(&maps.x, p, p.x, p.ldx) &&
+            map_tiles<NARROW, TG>(&maps.a, p, p.a, p.lda) &&
+            (!p.b || map_tiles<NARROW, TG>(&maps.b, p, p.b, p.ldb)) &&
+            map_tiles<NARROW, TD>(&maps.dh, p, p.dh, p.lddh);
+    // one block a channel: no sums to join
+    const bool alone = p.B == 1 && most_blocks(p, Shape<NARROW>::kT) == 1;
     const int vec = pairs(p.dx, p.lddx, sizeof(TD)) && pairs(p.da, p.ldda, sizeof(TDG)) &&
                     pairs(p.db, p.lddb, sizeof(TDG));
-    static KernelSlots known;
     int cs = 1;
-    cudaError_t e = launch_chains(linrec_bwd_kernel<TX, TG, GIVEN, SCALE, TD, TDG>,
-                                  sizeof(BwdSmem<TX, TG, TD>), p, c, &known, vec, &cs, s, maps,
-                                  states, alone ? nullptr : sums);
+    cudaError_t e = launch_chains<NARROW>(kernel, sizeof(BwdSmem<TX, TG, TD>), p, c, known, vec,
+                                          &cs, s, maps, states, alone ? nullptr : sums);
     if (e != cudaSuccess || GIVEN || alone) return e;
     linrec_sums_kernel<<<(p.D + 31) / 32, dim3(32, kSumRows), 0, s>>>(
         sums, (long long)p.B * cs, p.D, p.dA_log, p.ddt_bias);
@@ -342,7 +361,7 @@ size_t linrec_bwd_workspace_bytes(const long long* cu, int B, int T, int D, bool
   return (cu ? seq_table_bytes(B) : 0) + (states_given ? 0 : states_bytes(a)) +
          (flags & GDN_GATES_PRECOMPUTED
               ? 0
-              : align256((size_t)B * most_blocks(a) * D * sizeof(float2)));
+              : align256((size_t)B * most_blocks(a, kLinrecChunk) * D * sizeof(float2)));
 }
 
 cudaError_t launch_linrec_bwd(const LinrecArgs& a, void* workspace, cudaStream_t s) {

@@ -21,7 +21,7 @@ cudaError_t launch_linrec_scan(const LinrecArgs& a, const Chains& ch, int wide_f
                                cudaStream_t s);
 
 // The map of a tensor's tiles, where its rows start on 16 bytes.
-template <typename T>
+template <bool NARROW, typename T>
 bool map_tiles(CUtensorMap* m, const LinrecArgs& p, const void* base, long long ld) {
   if (((reinterpret_cast<uintptr_t>(base) | (uintptr_t)(ld * (long long)sizeof(T))) & 15) != 0)
     return false;
@@ -30,7 +30,7 @@ bool map_tiles(CUtensorMap* m, const LinrecArgs& p, const void* base, long long 
   const cuuint64_t rows = p.cu ? 1 : p.B;
   const cuuint64_t dims[3] = {(cuuint64_t)p.D, (cuuint64_t)p.T, rows};
   const cuuint64_t strides[2] = {(cuuint64_t)ld * sizeof(T), (cuuint64_t)p.T * ld * sizeof(T)};
-  const cuuint32_t box[3] = {kTileC, kTileT, 1}, es[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {Shape<NARROW>::kC, Shape<NARROW>::kT, 1}, es[3] = {1, 1, 1};
   return enc(m, sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
              3, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -41,25 +41,32 @@ inline int pairs(const void* p, long long ld, int es) {
   return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(ld * es)) & (2 * es - 1)) == 0;
 }
 
+// Tokens of the longest sequence.
+inline long long longest(const LinrecArgs& p) {
+  if (p.cu == nullptr) return p.T;
+  long long n = 0;
+  for (int i = 0; i < p.B; ++i) n = p.cu[i + 1] - p.cu[i] > n ? p.cu[i + 1] - p.cu[i] : n;
+  return n;
+}
 // The most blocks that one chain can use.
-inline int most_blocks(const LinrecArgs& p) {
-  long long longest = p.T;
-  if (p.cu) {
-    longest = 0;
-    for (int i = 0; i < p.B; ++i)
-      longest = p.cu[i + 1] - p.cu[i] > longest ? p.cu[i + 1] - p.cu[i] : longest;
-  }
+inline int most_blocks(const LinrecArgs& p, int tile_tokens) {
+  const long long n = longest(p);
   int cs = 1;
-  while (cs < kMaxCluster && (long long)cs * kTileT < longest) cs *= 2;
+  while (cs < kMaxCluster && (long long)cs * tile_tokens < n) cs *= 2;
   return cs;
 }
 // Blocks of a cluster: as many as still leave every block of the launch a place on the
 // machine (`slots` blocks run at once).
-inline int cluster_size(const LinrecArgs& p, long long chains, int slots) {
-  const int most = most_blocks(p);
+inline int cluster_size(const LinrecArgs& p, int tile_tokens, long long chains, int slots) {
+  const int most = most_blocks(p, tile_tokens);
   int cs = 1;
   while (cs < most && chains * cs * 2 <= slots) cs *= 2;
   return cs;
+}
+// Whether the tiles are narrow: where the chains of 64 channels do not fill the machine and
+// a sequence is longer than a chunk.
+inline bool narrow_tiles(const LinrecArgs& p, int slots) {
+  return (long long)p.B * ((p.D + 63) / 64) < slots && longest(p) > kLinrecChunk;
 }
 
 // What the runtime says of one kernel on this device, asked once: blocks that run at once
@@ -88,7 +95,7 @@ cudaError_t kernel_slots(K kernel, size_t smem, KernelSlots* known, int* slots) 
   return cudaSuccess;
 }
 
-template <typename K, typename... More>
+template <bool NARROW, typename K, typename... More>
 cudaError_t launch_chains(K kernel, size_t smem, const LinrecArgs& p, const Chains& chains,
                           KernelSlots* known, int vec, int* cluster, cudaStream_t s,
                           More... more) {
@@ -96,8 +103,9 @@ cudaError_t launch_chains(K kernel, size_t smem, const LinrecArgs& p, const Chai
   cudaError_t e = kernel_slots(kernel, smem, known, &slots);
   if (e != cudaSuccess) return e;
   Chains ch = chains;
+  ch.nblk = (p.D + Shape<NARROW>::kC - 1) / Shape<NARROW>::kC;
   const long long n = (long long)p.B * ch.nblk;
-  ch.cs = cluster_size(p, n, slots);
+  ch.cs = cluster_size(p, Shape<NARROW>::kT, n, slots);
   *cluster = ch.cs;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -107,7 +115,7 @@ cudaError_t launch_chains(K kernel, size_t smem, const LinrecArgs& p, const Chai
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(n * ch.cs));
   cfg.blockDim = dim3(kLinrecThreads);
-  cfg.dynamicSmemBytes = smem + (ch.cs > 1 ? 2 * ch.cs * sizeof(FoldRow) : 0);
+  cfg.dynamicSmemBytes = smem + (ch.cs > 1 || NARROW ? 2 * ch.cs * sizeof(FoldRow) : 0);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = ch.cs > 1 ? 1 : 0;

@@ -1,16 +1,16 @@
 // linrec_tile.cuh -- what the scan of the gated linear recurrence and the reverse scan of
-// its backward share: tiles of 64 tokens x 64 channels, their rows copied to shared memory
-// ahead of use, and the carry from tile to tile.
+// its backward share: tiles of tokens x channels, their rows copied to shared memory ahead of
+// use, and the carry from tile to tile.
 //
-// A chain is one sequence's 64 channels; its tiles are taken in turn by the blocks of one
-// thread-block cluster (1 to 16 blocks: as many as it takes to fill the machine).  A tile is
-// 8 warps x 8 tokens; a lane holds 2 adjacent channels.  Each thread folds its 8 tokens into
-// (A, H): carry_out = A carry_in + H; the folds of the 8 warps meet in shared memory, so that
-// within a tile the recurrence is 8 + 8 steps instead of 64.  The blocks of a cluster send
-// their tiles' (A, H) to one another through distributed shared memory, counted on the
-// receiver's mbarrier, and each runs the same carry through the tiles of the round.  The
-// carry is folded tile by tile in order whatever the cluster's size, so the result does not
-// depend on it.
+// A chain is one sequence's 64 channels (or 32: Shape); its tiles are taken in turn by the
+// blocks of one thread-block cluster (1 to 16 blocks: as many as it takes to fill the
+// machine).  A lane holds 2 adjacent channels of 8 tokens.  Each thread folds its 8 tokens
+// into (A, H): carry_out = A carry_in + H; the folds of a chunk's 8 groups of tokens meet in
+// shared memory, so that within a chunk the recurrence is 8 + 8 steps instead of 64.  The
+// blocks of a cluster send their chunks' (A, H) to one another through distributed shared
+// memory, counted on the receiver's mbarrier, and each runs the same carry through the chunks
+// of the round.  The carry is folded chunk by chunk in order whatever the cluster's size and
+// the tile's shape, so the result does not depend on them.
 #pragma once
 
 #include "common.cuh"
@@ -22,13 +22,42 @@
 
 namespace gdn {
 
-constexpr int kTileT = kLinrecChunk;  // tokens of a tile
-constexpr int kTileC = 64;            // channels of a tile
-constexpr int kWarps = 8;             // of a block, 8 tokens each
-constexpr int kPer = kTileT / kWarps;
+constexpr int kWarps = 8;   // of a block
+constexpr int kPer = 8;     // tokens of a thread
 constexpr int kLinrecThreads = kWarps * 32;
 constexpr int kMaxCluster = 16;
-constexpr int kGroup = 4;             // tokens whose gates are formed together
+constexpr int kGroup = 4;   // tokens whose gates are formed together
+constexpr int kTile = 64 * 64;  // elements of a tile
+
+// A tile's shape: one chunk of 64 channels, or two chunks of 32 where there are few chains to
+// share the machine (half the channels are twice the chains, and half the rounds of the
+// cluster; its rows are 64 bytes of bf16 instead of 128).
+template <bool NARROW>
+struct Shape {
+  static constexpr int kChunks = NARROW ? 2 : 1;
+  static constexpr int kT = kChunks * kLinrecChunk, kC = 64 / kChunks;
+  static constexpr int kLanes = kC / 2;  // of one group of tokens
+};
+// A thread's place in it.
+template <bool NARROW>
+struct Spot {
+  int lane, warp, cl, half, first;  // channel pair, the warp's lower or upper lanes, first token
+  __device__ __forceinline__ Spot() {
+    constexpr int kLanes = Shape<NARROW>::kLanes;
+    lane = threadIdx.x & 31;
+    warp = threadIdx.x / 32;
+    cl = lane % kLanes;
+    half = lane / kLanes;
+    first = (threadIdx.x / kLanes) * kPer;
+  }
+  // first element of the thread in a tile
+  __device__ __forceinline__ int mine() const { return first * Shape<NARROW>::kC + 2 * cl; }
+  // For the joining warps, whose upper lanes (NARROW) take the second chunk: where group w of
+  // the lane's chunk has its fold.
+  __device__ __forceinline__ int group(int w) const {
+    return (half * 8 + w) * Shape<NARROW>::kLanes + cl;
+  }
+};
 
 // Packed batches: each sequence's first token and first chunk, entry B the totals.
 struct SeqTab {
@@ -58,32 +87,34 @@ struct Chain {
   long long len;   // its tokens
   long long chunk0;
   int row, c0;     // sequence, first channel
-  int chunks, rank;
+  int chunks, tiles, rank;
 };
+template <bool NARROW>
 __device__ __forceinline__ Chain chain_of(const LinrecArgs& p, const Chains& ch) {
   Chain k;
   const int id = blockIdx.x / ch.cs;
   k.rank = blockIdx.x % ch.cs;
   k.row = id / ch.nblk;
-  k.c0 = (id - k.row * ch.nblk) * kTileC;
+  k.c0 = (id - k.row * ch.nblk) * Shape<NARROW>::kC;
   if (ch.tab.cu == nullptr) {
     k.tok = (long long)k.row * p.T;
     k.len = p.T;
-    k.chunk0 = (long long)k.row * ((p.T + (long long)kTileT - 1) / kTileT);
+    k.chunk0 = (long long)k.row * ((p.T + (long long)kLinrecChunk - 1) / kLinrecChunk);
   } else {
     k.tok = ch.tab.cu[k.row];
     k.len = ch.tab.cu[k.row + 1] - k.tok;
     k.chunk0 = ch.tab.chunk0[k.row];
   }
-  k.chunks = (int)((k.len + kTileT - 1) / kTileT);
+  k.chunks = (int)((k.len + kLinrecChunk - 1) / kLinrecChunk);
+  k.tiles = (k.chunks + Shape<NARROW>::kChunks - 1) / Shape<NARROW>::kChunks;
   return k;
 }
 
 // Shared memory of the carry: each warp's fold, the carry into the tile, and behind the
 // kernel's own shared memory the cluster's folds, [2 rounds][cs][32].
 struct CarrySmem {
-  float4 fold[kWarps][32];   // (A, A', H, H') of a lane's two channels
-  float2 start[kWarps][32];  // what enters each warp's tokens
+  float4 fold[kLinrecThreads];   // (A, A', H, H') of each thread's two channels
+  float2 start[kLinrecThreads];  // what enters its tokens
   uint64_t full[2];          // the round's folds have arrived
   uint64_t loaded[2];        // the stage's tiles have
 };
@@ -103,35 +134,51 @@ __device__ __forceinline__ void st_async_peer(uint32_t addr, float4 v, uint32_t 
       : "memory");
 }
 
-// One round of the carry, by one warp: own is this block's tile's (A, H).  Returns what
-// enters the tile and moves `carry` behind the round's last tile.  `lost`: a wait has
-// expired, later ones are not tried.
+// One round of the carry, by one warp: own is the (A, H) of the lane's chunk of this block's
+// tile.  Returns what enters that chunk and moves `carry` behind the round's last chunk; BACK:
+// a tile's second chunk comes first.  `lost`: a wait has expired, later ones are not tried.
+template <bool NARROW, bool BACK>
 __device__ __forceinline__ float2 carry_round(const Chains& ch, int rank, int round, float4 own,
                                               CarrySmem& sm, FoldRow* folds, float2* carry,
                                               bool* lost) {
-  if (ch.cs == 1) {
-    const float2 in = *carry;
+  const int lane = threadIdx.x & 31, buf = round & 1;
+  FoldRow* row = folds + buf * ch.cs;
+  if (ch.cs > 1) {
+    if (lane == 0)
+      tc::mbar_arrive_expect_tx(&sm.full[buf], (uint32_t)(ch.cs * 32 * sizeof(float4)));
+    __syncwarp();
+    if (!*lost && !(ch.fault && rank == 0))  // nothing is under way to a peer that has given up
+      for (int r = 0; r < ch.cs; ++r)
+        st_async_peer(tc::map_peer(&row[rank][lane], r), own, tc::map_peer(&sm.full[buf], r));
+    if (!*lost) {
+      const bool ok = tc::mbar_wait(&sm.full[buf], (round >> 1) & 1, nullptr, 0, ch.spin);
+      *lost = !__all_sync(0xffffffffu, ok);
+      if (*lost && lane == 0) report_timeout(ch.status, 0x4c52);
+    }
+  } else if (NARROW) {  // the lanes' two chunks
+    row[0][lane] = own;
+    __syncwarp();
+  }
+  float2 in = *carry, v = *carry;
+  if (!NARROW && ch.cs == 1) {
     *carry = fma2(first2(own), in, last2(own));
     return in;
   }
-  const int lane = threadIdx.x & 31, buf = round & 1;
-  FoldRow* row = folds + buf * ch.cs;
-  if (lane == 0)
-    tc::mbar_arrive_expect_tx(&sm.full[buf], (uint32_t)(ch.cs * 32 * sizeof(float4)));
-  __syncwarp();
-  if (!*lost && !(ch.fault && rank == 0))  // nothing is under way to a peer that has given up
-    for (int r = 0; r < ch.cs; ++r)
-      st_async_peer(tc::map_peer(&row[rank][lane], r), own, tc::map_peer(&sm.full[buf], r));
-  if (!*lost) {
-    const bool ok = tc::mbar_wait(&sm.full[buf], (round >> 1) & 1, nullptr, 0, ch.spin);
-    *lost = !__all_sync(0xffffffffu, ok);
-    if (*lost && lane == 0) report_timeout(ch.status, 0x4c52);
-  }
-  float2 in = *carry, v = *carry;
+  const int half = lane / 16, cl = lane % 16;
   for (int r = 0; r < ch.cs; ++r) {
-    if (r == rank) in = v;
-    const float4 f = row[r][lane];
-    v = fma2(first2(f), v, last2(f));
+    if (NARROW) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int h = BACK ? 1 - i : i;
+        if (r == rank && h == half) in = v;
+        const float4 f = row[r][16 * h + cl];
+        v = fma2(first2(f), v, last2(f));
+      }
+    } else {
+      if (r == rank) in = v;
+      const float4 f = row[r][lane];
+      v = fma2(first2(f), v, last2(f));
+    }
   }
   *carry = v;
   return in;
@@ -154,7 +201,7 @@ __device__ __forceinline__ void carry_end(const Chains& ch) {
   if (ch.cs > 1) tc::cluster_sync();
 }
 
-// Tiles of one tensor to shared memory [64][64].  Tensors whose rows start on 16 bytes come
+// Tiles of one tensor to shared memory [tokens][channels].  Tensors whose rows start on 16 bytes come
 // by TMA, one instruction a tile, through a map over [channels][tokens][rows of the batch]
 // (zeros behind the last token of a dense row and behind the last channel); the tokens behind
 // a packed sequence are the next one's and are cleared by the caller.
@@ -179,9 +226,10 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-template <typename T>
+template <bool NARROW, typename T>
 __device__ __forceinline__ void load_elements(T* dst, const void* base, long long ld,
                                               long long tok, int n, int c0, int D) {
+  constexpr int kTileC = Shape<NARROW>::kC, kTileT = Shape<NARROW>::kT;
   constexpr int kStep = kLinrecThreads / kTileC;  // rows at once
   const int r0 = threadIdx.x / kTileC, c = threadIdx.x % kTileC;
   const bool in = c < D - c0;
@@ -198,9 +246,9 @@ __device__ __forceinline__ void load_elements(T* dst, const void* base, long lon
   }
 }
 // Clears the rows of a tile behind its n tokens.
-template <typename T>
+template <bool NARROW, typename T>
 __device__ __forceinline__ void clear_rows(T* tile, int n) {
-  for (int i = n * kTileC + threadIdx.x; i < kTileT * kTileC; i += kLinrecThreads)
+  for (int i = n * Shape<NARROW>::kC + threadIdx.x; i < kTile; i += kLinrecThreads)
     tile[i] = from_f32<T>(0.f);
 }
 
@@ -221,7 +269,7 @@ __device__ __forceinline__ void put2(T* p, float2 v, int cols) {
   if (cols > 1) p[1] = from_f32<T>(v.y);
 }
 // An output tensor of a block: a 64-bit base that moves from tile to tile, the same for all
-// threads, and 32-bit byte offsets inside a tile (64 rows of at most 2^23 elements).
+// threads, and 32-bit byte offsets inside a tile (128 rows of at most 2^22 elements).
 template <typename T>
 struct Rows {
   char* base;
