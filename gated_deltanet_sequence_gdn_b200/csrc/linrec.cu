@@ -246,10 +246,11 @@ struct FwdRun {
     using TO = typename Wide<TX, WIDE>::type;
     static KernelSlots known, known_narrow;
     const auto kernel = linrec_fwd_kernel<TX, TG, GIVEN, SCALE, TO, false>;
-    int slots = 0, cs = 1;
+    const std::atomic<int>* slots = nullptr;
+    int cs = 1;
     cudaError_t e = kernel_slots(kernel, sizeof(FwdSmem<TX, TG>), &known, &slots);
     if (e != cudaSuccess) return e;
-    return narrow_tiles(p, slots)
+    return narrow_tiles(p, slots[0].load(std::memory_order_relaxed))
                ? launch<TX, TG, true>(linrec_fwd_kernel<TX, TG, GIVEN, SCALE, TO, true>,
                                       &known_narrow, &cs)
                : launch<TX, TG, false>(kernel, &known, &cs);

@@ -315,10 +315,10 @@ struct BwdRun {
     using TDG = typename Wide<TD, GIVEN>::type;
     static KernelSlots known, known_narrow;
     const auto kernel = linrec_bwd_kernel<TX, TG, GIVEN, SCALE, TD, TDG, false>;
-    int slots = 0;
+    const std::atomic<int>* slots = nullptr;
     cudaError_t e = kernel_slots(kernel, sizeof(BwdSmem<TX, TG, TD>), &known, &slots);
     if (e != cudaSuccess) return e;
-    return narrow_tiles(p, slots)
+    return narrow_tiles(p, slots[0].load(std::memory_order_relaxed))
                ? launch<TX, TG, GIVEN, TD, TDG, true>(
                      linrec_bwd_kernel<TX, TG, GIVEN, SCALE, TD, TDG, true>, &known_narrow)
                : launch<TX, TG, GIVEN, TD, TDG, false>(kernel, &known);

@@ -55,12 +55,19 @@ inline int most_blocks(const LinrecArgs& p, int tile_tokens) {
   while (cs < kMaxCluster && (long long)cs * tile_tokens < n) cs *= 2;
   return cs;
 }
-// Blocks of a cluster: as many as still leave every block of the launch a place on the
-// machine (`slots` blocks run at once).
-inline int cluster_size(const LinrecArgs& p, int tile_tokens, long long chains, int slots) {
+// What the runtime says of one kernel on one device, asked once: the clusters of 1, 2, 4, 8
+// and 16 blocks that run at once (at[0]: 0 until asked).
+struct KernelSlots {
+  std::atomic<int> at[64][5];
+};
+// Blocks of a cluster (as a power of two): as many as still let every cluster of the launch
+// run at once.
+inline int cluster_size(const LinrecArgs& p, int tile_tokens, long long chains,
+                        const std::atomic<int>* slots) {
   const int most = most_blocks(p, tile_tokens);
   int cs = 1;
-  while (cs < most && chains * cs * 2 <= slots) cs *= 2;
+  for (int j = 1; j < 5 && cs < most; ++j)
+    if (chains <= slots[j].load(std::memory_order_relaxed) && (1 << j) <= most) cs = 1 << j;
   return cs;
 }
 // Whether the tiles are narrow: where the chains of 64 channels do not fill the machine and
@@ -69,18 +76,15 @@ inline bool narrow_tiles(const LinrecArgs& p, int slots) {
   return (long long)p.B * ((p.D + 63) / 64) < slots && longest(p) > kLinrecChunk;
 }
 
-// What the runtime says of one kernel on this device, asked once: blocks that run at once
-// (0: not asked yet).
-struct KernelSlots {
-  std::atomic<int> at[64];
-};
 template <typename K>
-cudaError_t kernel_slots(K kernel, size_t smem, KernelSlots* known, int* slots) {
+cudaError_t kernel_slots(K kernel, size_t smem, KernelSlots* known, const std::atomic<int>** slots) {
   int dev = 0, sms = 0, per = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const bool keep = dev < 64;
-  if (keep && (*slots = known->at[dev].load(std::memory_order_acquire)) != 0) return cudaSuccess;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::atomic<int>* at = known->at[dev];
+  *slots = at;
+  if (at[0].load(std::memory_order_acquire) != 0) return cudaSuccess;
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const size_t most = smem + 2 * kMaxCluster * sizeof(FoldRow);
   if (e == cudaSuccess)
@@ -90,8 +94,25 @@ cudaError_t kernel_slots(K kernel, size_t smem, KernelSlots* known, int* slots) 
   if (e == cudaSuccess)
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kLinrecThreads, smem);
   if (e != cudaSuccess) return e;
-  *slots = sms * (per > 0 ? per : 1);
-  if (keep) known->at[dev].store(*slots, std::memory_order_release);
+  for (int j = 1; j < 5; ++j) {
+    const int cs = 1 << j;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cs;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(sms * 8 / cs * cs));
+    cfg.blockDim = dim3(kLinrecThreads);
+    cfg.dynamicSmemBytes = smem + 2 * cs * sizeof(FoldRow);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    at[j].store(n, std::memory_order_relaxed);
+  }
+  at[0].store(sms * (per > 0 ? per : 1), std::memory_order_release);
   return cudaSuccess;
 }
 
@@ -99,7 +120,7 @@ template <bool NARROW, typename K, typename... More>
 cudaError_t launch_chains(K kernel, size_t smem, const LinrecArgs& p, const Chains& chains,
                           KernelSlots* known, int vec, int* cluster, cudaStream_t s,
                           More... more) {
-  int slots = 0;
+  const std::atomic<int>* slots = nullptr;
   cudaError_t e = kernel_slots(kernel, smem, known, &slots);
   if (e != cudaSuccess) return e;
   Chains ch = chains;
