@@ -530,8 +530,8 @@ static int validate_linrec(const LinrecArgs& p, int more_flags, long long* chunk
       if (p.cu[i + 1] < p.cu[i]) return GDN_ERR_INVALID_ARG;
   }
   *chunks = linrec_chunks(p.cu, p.B, p.T);
-  // chunk and tile numbers are 32-bit, and so are byte offsets inside a tile of 128 tokens
-  if (p.ldx > 1 << 22 || p.lda > 1 << 22 || p.ldb > 1 << 22 || p.D > 1 << 22)
+  // chunk and tile numbers are 32-bit, and so are byte offsets inside a tile of 256 tokens
+  if (p.ldx > 1 << 21 || p.lda > 1 << 21 || p.ldb > 1 << 21 || p.D > 1 << 21)
     return GDN_ERR_UNSUPPORTED;
   if (*chunks * ((p.D + 31) / 32) > 0x3fffffffLL) return GDN_ERR_UNSUPPORTED;
   if (p.B == 0 || *chunks == 0) return GDN_OK;
@@ -582,7 +582,7 @@ int gdn_linrec_fwd(const void* x, const void* a, const void* b, const float* A_l
   if (chunks == 0) return from_cuda(launch_copy_state(h0, ht, (size_t)B * D, s));
   if (!ok_elem(h, (flags & GDN_OUT_F32) ? 4 : elem_size(dtype)) || ldh < D)
     return GDN_ERR_INVALID_ARG;
-  if (ldh > 1 << 22) return GDN_ERR_UNSUPPORTED;
+  if (ldh > 1 << 21) return GDN_ERR_UNSUPPORTED;
   if (!ok_workspace(workspace, ws_bytes, linrec_workspace_bytes(cu_seqlens, B, T, D)))
     return GDN_ERR_WORKSPACE;
   return from_cuda(launch_linrec_fwd(p, workspace, s));
@@ -620,7 +620,7 @@ int gdn_linrec_bwd(const void* x, const void* a, const void* b, const float* A_l
   if (!ok_elem(dh, ds) || lddh < D || !ok_elem(dx, ds) || lddx < D || !ok_elem(da, gs) ||
       ldda < D || (db != nullptr && (!ok_elem(db, gs) || lddb < D)))
     return GDN_ERR_INVALID_ARG;
-  if (lddh > 1 << 22 || lddx > 1 << 22 || ldda > 1 << 22 || lddb > 1 << 22)
+  if (lddh > 1 << 21 || lddx > 1 << 21 || ldda > 1 << 21 || lddb > 1 << 21)
     return GDN_ERR_UNSUPPORTED;
   if (!ok_workspace(workspace, ws_bytes,
                     linrec_bwd_workspace_bytes(cu_seqlens, B, T, D, states != nullptr, flags)))

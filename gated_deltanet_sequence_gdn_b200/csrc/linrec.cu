@@ -15,27 +15,38 @@ long long linrec_chunks(const long long* cu, int B, int T) {
 
 namespace {
 
+// Shared memory: the carry, then two stages of x, a and (where there is a write gate) b, then
+// the cluster's folds.
+template <typename TX, typename TG>
+constexpr size_t stage_bytes(bool gate) {
+  return kTile * (sizeof(TX) + sizeof(TG) * (gate ? 2 : 1));
+}
+constexpr size_t kCarryBytes = (sizeof(CarrySmem) + 127) / 128 * 128;
+template <typename TX, typename TG>
+constexpr size_t fwd_smem(bool gate) {
+  return kCarryBytes + 2 * stage_bytes<TX, TG>(gate);
+}
 template <typename TX, typename TG>
 struct FwdStage {
-  alignas(128) TX x[kTile];
-  alignas(128) TG a[kTile];
-  alignas(128) TG b[kTile];
-};
-template <typename TX, typename TG>
-struct FwdSmem {
-  FwdStage<TX, TG> stage[2];
-  CarrySmem carry;
+  TX* x;
+  TG *a, *b;
 };
 
-template <typename TX, typename TG, bool GIVEN, int SCALE, typename TO, bool NARROW>
+template <typename TX, typename TG, bool GIVEN, int SCALE, typename TO, int SPLIT>
 __global__ void __launch_bounds__(kLinrecThreads, sizeof(TX) + sizeof(TG) == 4 ? 4 : 2)
 linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ LinrecMaps maps) {
   extern __shared__ __align__(128) unsigned char smem_raw[];
-  auto& sm = *reinterpret_cast<FwdSmem<TX, TG>*>(smem_raw);
-  FoldRow* folds = reinterpret_cast<FoldRow*>(smem_raw + sizeof(FwdSmem<TX, TG>));
-  constexpr int kTileT = Shape<NARROW>::kT, kC = Shape<NARROW>::kC, kTileChunks = kTileT / kLinrecChunk;
-  const Spot<NARROW> at;
-  const Chain k = chain_of<NARROW>(p, ch);
+  CarrySmem& carry_sm = *reinterpret_cast<CarrySmem*>(smem_raw);
+  const uint32_t stage_size = stage_bytes<TX, TG>(p.b != nullptr);
+  FoldRow* folds = reinterpret_cast<FoldRow*>(smem_raw + kCarryBytes + 2 * stage_size);
+  auto stage = [&](int round) {
+    unsigned char* s = smem_raw + kCarryBytes + (round & 1) * stage_size;
+    TG* a = reinterpret_cast<TG*>(s + kTile * sizeof(TX));
+    return FwdStage<TX, TG>{reinterpret_cast<TX*>(s), a, a + kTile};
+  };
+  constexpr int kTileT = Shape<SPLIT>::kT, kC = Shape<SPLIT>::kC, kTileChunks = kTileT / kLinrecChunk;
+  const Spot<SPLIT> at;
+  const Chain k = chain_of<SPLIT>(p, ch);
   const int c = k.c0 + 2 * at.cl, cols = p.D - c;
   const int step = ch.cs * kTileT;
   const int tokens = (int)k.len - k.rank * kTileT;  // from the block's first tile on
@@ -45,26 +56,26 @@ linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
   };
   auto load = [&](int round) {
     const int n = length(round), t = (round * ch.cs + k.rank) * kTileT;
-    FwdStage<TX, TG>& st = sm.stage[round & 1];
+    const FwdStage<TX, TG> st = stage(round);
     if (ch.tma) {
       if (n > 0 && threadIdx.x == 0) {
-        uint64_t* bar = &sm.carry.loaded[round & 1];
+        uint64_t* bar = &carry_sm.loaded[round & 1];
         const int y = ch.tab.cu ? (int)k.tok + t : t, z = ch.tab.cu ? 0 : k.row;
-        tc::mbar_arrive_expect_tx(bar, sizeof(st.x) + sizeof(st.a) + (p.b ? sizeof(st.b) : 0));
+        tc::mbar_arrive_expect_tx(bar, stage_size);
         tma_load_3d(st.x, &maps.x, bar, k.c0, y, z);
         tma_load_3d(st.a, &maps.a, bar, k.c0, y, z);
         if (p.b) tma_load_3d(st.b, &maps.b, bar, k.c0, y, z);
       }
     } else {
       if (n > 0) {
-        load_elements<NARROW>(st.x, p.x, p.ldx, k.tok + t, n, k.c0, p.D);
-        load_elements<NARROW>(st.a, p.a, p.lda, k.tok + t, n, k.c0, p.D);
-        if (p.b) load_elements<NARROW>(st.b, p.b, p.ldb, k.tok + t, n, k.c0, p.D);
+        load_elements<SPLIT>(st.x, p.x, p.ldx, k.tok + t, n, k.c0, p.D);
+        load_elements<SPLIT>(st.a, p.a, p.lda, k.tok + t, n, k.c0, p.D);
+        if (p.b) load_elements<SPLIT>(st.b, p.b, p.ldb, k.tok + t, n, k.c0, p.D);
       }
       cp_async_commit();
     }
   };
-  carry_begin(ch, sm.carry);
+  carry_begin(ch, carry_sm);
   load(0);
   GateConst gc{both(0.f), both(0.f)};
   if (!GIVEN) gc = gate_const(p.A_log, p.dt_bias, c, p.D);
@@ -77,12 +88,12 @@ linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
     const int n = length(round);
     if (!ch.tma) {
       cp_async_wait<0>();
-    } else if (n > 0 && !tc::mbar_wait(&sm.carry.loaded[round & 1], (round >> 1) & 1, nullptr, 0)) {
+    } else if (n > 0 && !tc::mbar_wait(&carry_sm.loaded[round & 1], (round >> 1) & 1, nullptr, 0)) {
       report_timeout(ch.status, 0x4c54);
     }
     __syncthreads();  // the stage is complete, the other one free
     if (round + 1 < rounds) load(round + 1);
-    const FwdStage<TX, TG>& st = sm.stage[round & 1];
+    const FwdStage<TX, TG> st = stage(round);
     const int mine = at.mine();
     float2 al[kPer], u[kPer];
 #pragma unroll
@@ -125,32 +136,32 @@ linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
       H = fma2(al[i], H, u[i]);
       A = mul2(A, al[i]);
     }
-    sm.carry.fold[threadIdx.x] = join4(A, H);
+    carry_sm.fold[threadIdx.x] = join4(A, H);
     __syncthreads();
     if (at.warp == 0) {
       A = both(1.f);
       H = both(0.f);
 #pragma unroll 4
       for (int w = 0; w < 8; ++w) {
-        const float4 f = sm.carry.fold[at.group(w)];
+        const float4 f = carry_sm.fold[at.group(w)];
         H = fma2(first2(f), H, last2(f));
         A = mul2(A, first2(f));
       }
-      float2 v = carry_round<NARROW, false>(ch, k.rank, round, join4(A, H), sm.carry, folds, &carry,
+      float2 v = carry_round<SPLIT, false>(ch, k.rank, round, join4(A, H), carry_sm, folds, &carry,
                                             &lost);
-      if (n > at.half * kLinrecChunk)
+      if (n > at.part * kLinrecChunk)
         write2(p.states_out,
-               k.chunk0 + (long long)(round * ch.cs + k.rank) * kTileChunks + at.half, c, p.D, v);
+               k.chunk0 + (long long)(round * ch.cs + k.rank) * kTileChunks + at.part, c, p.D, v);
 #pragma unroll 4
       for (int w = 0; w < 8; ++w) {
-        sm.carry.start[at.group(w)] = v;
-        const float4 f = sm.carry.fold[at.group(w)];
+        carry_sm.start[at.group(w)] = v;
+        const float4 f = carry_sm.fold[at.group(w)];
         v = fma2(first2(f), v, last2(f));
       }
     }
     __syncthreads();
     if (p.h) {
-      float2 h = sm.carry.start[threadIdx.x];
+      float2 h = carry_sm.start[threadIdx.x];
       if (n == kTileT && cols > 1 && vec) {
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
@@ -167,7 +178,7 @@ linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
       out.advance(step);
     }
   }
-  if (k.rank == 0 && at.warp == 0 && at.half == 0) write2(p.ht, k.row, c, p.D, carry);
+  if (k.rank == 0 && at.warp == 0 && at.part == 0) write2(p.ht, k.row, c, p.D, carry);
   carry_end(ch);
 }
 
@@ -244,25 +255,27 @@ struct FwdRun {
   template <typename TX, typename TG, bool GIVEN, int SCALE, bool WIDE>
   cudaError_t run() const {
     using TO = typename Wide<TX, WIDE>::type;
-    static KernelSlots known, known_narrow;
-    const auto kernel = linrec_fwd_kernel<TX, TG, GIVEN, SCALE, TO, false>;
-    const std::atomic<int>* slots = nullptr;
-    int cs = 1;
-    cudaError_t e = kernel_slots(kernel, sizeof(FwdSmem<TX, TG>), &known, &slots);
+    static KernelSlots known[2][3];  // with and without a write gate
+    KernelSlots* k = known[p.b != nullptr];
+    const auto k1 = linrec_fwd_kernel<TX, TG, GIVEN, SCALE, TO, 1>;
+    const auto k2 = linrec_fwd_kernel<TX, TG, GIVEN, SCALE, TO, 2>;
+    const auto k4 = linrec_fwd_kernel<TX, TG, GIVEN, SCALE, TO, 4>;
+    Split sp;
+    cudaError_t e = choose_split(p, k1, k2, k4, fwd_smem<TX, TG>(p.b != nullptr),
+                                 fwd_smem<TX, TG>(true), k, &sp);
     if (e != cudaSuccess) return e;
-    return narrow_tiles(p, slots[0].load(std::memory_order_relaxed))
-               ? launch<TX, TG, true>(linrec_fwd_kernel<TX, TG, GIVEN, SCALE, TO, true>,
-                                      &known_narrow, &cs)
-               : launch<TX, TG, false>(kernel, &known, &cs);
+    return sp.split == 4   ? launch<TX, TG, 4>(k4, sp.cs)
+           : sp.split == 2 ? launch<TX, TG, 2>(k2, sp.cs)
+                           : launch<TX, TG, 1>(k1, sp.cs);
   }
-  template <typename TX, typename TG, bool NARROW, typename K>
-  cudaError_t launch(K kernel, KernelSlots* known, int* cs) const {
+  template <typename TX, typename TG, int SPLIT, typename K>
+  cudaError_t launch(K kernel, int cs) const {
     LinrecMaps maps;
     Chains c = ch;
-    c.tma = map_tiles<NARROW, TX>(&maps.x, p, p.x, p.ldx) &&
-            map_tiles<NARROW, TG>(&maps.a, p, p.a, p.lda) &&
-            (!p.b || map_tiles<NARROW, TG>(&maps.b, p, p.b, p.ldb));
-    return launch_chains<NARROW>(kernel, sizeof(FwdSmem<TX, TG>), p, c, known, vec, cs, s, maps);
+    c.tma = map_tiles<SPLIT, TX>(&maps.x, p, p.x, p.ldx) &&
+            map_tiles<SPLIT, TG>(&maps.a, p, p.a, p.lda) &&
+            (!p.b || map_tiles<SPLIT, TG>(&maps.b, p, p.b, p.ldb));
+    return launch_chains<SPLIT>(kernel, fwd_smem<TX, TG>(p.b != nullptr), p, c, cs, vec, s, maps);
   }
 };
 struct StepRun {

@@ -34,7 +34,7 @@ __device__ __forceinline__ void add_kept(float2* sum, float2* err, float2 v) {
   *sum = t;
 }
 
-template <typename TX, typename TG, bool GIVEN, int SCALE, typename TD, typename TDG, bool NARROW>
+template <typename TX, typename TG, bool GIVEN, int SCALE, typename TD, typename TDG, int SPLIT>
 __global__ void __launch_bounds__(kLinrecThreads, 2)
 linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ LinrecMaps maps,
                   const float* states, float2* sums) {
@@ -43,10 +43,10 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
   constexpr int kStages = Smem::kStages;
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
   FoldRow* folds = reinterpret_cast<FoldRow*>(smem_raw + sizeof(Smem));
-  constexpr int kTileT = Shape<NARROW>::kT, kC = Shape<NARROW>::kC, kTileChunks = kTileT / kLinrecChunk;
-  const Spot<NARROW> at;
+  constexpr int kTileT = Shape<SPLIT>::kT, kC = Shape<SPLIT>::kC, kTileChunks = kTileT / kLinrecChunk;
+  const Spot<SPLIT> at;
   const int first = at.first;
-  const Chain k = chain_of<NARROW>(p, ch);
+  const Chain k = chain_of<SPLIT>(p, ch);
   const int c = k.c0 + 2 * at.cl, cols = p.D - c;
   const int step = ch.cs * kTileT;
   const int last = k.tiles - 1 - k.rank;  // the block's first tile; may be before the sequence
@@ -72,10 +72,10 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
       }
     } else {
       if (n > 0) {
-        load_elements<NARROW>(st.x, p.x, p.ldx, k.tok + t, n, k.c0, p.D);
-        load_elements<NARROW>(st.a, p.a, p.lda, k.tok + t, n, k.c0, p.D);
-        if (p.b) load_elements<NARROW>(st.b, p.b, p.ldb, k.tok + t, n, k.c0, p.D);
-        load_elements<NARROW>(st.dh, p.dh, p.lddh, k.tok + t, n, k.c0, p.D);
+        load_elements<SPLIT>(st.x, p.x, p.ldx, k.tok + t, n, k.c0, p.D);
+        load_elements<SPLIT>(st.a, p.a, p.lda, k.tok + t, n, k.c0, p.D);
+        if (p.b) load_elements<SPLIT>(st.b, p.b, p.ldb, k.tok + t, n, k.c0, p.D);
+        load_elements<SPLIT>(st.dh, p.dh, p.lddh, k.tok + t, n, k.c0, p.D);
       }
       cp_async_commit();
     }
@@ -87,7 +87,7 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
   float2 carry = read2(p.dht, k.row, c, p.D);  // behind the round's last tile (warp 0's)
   bool lost = false;
   auto state = [&](int tt) {  // before the lane's chunk of a tile
-    const int j = tt * kTileChunks + at.half;
+    const int j = tt * kTileChunks + at.part;
     return tt >= 0 && j < k.chunks ? read2(states, k.chunk0 + j, c, p.D) : both(0.f);
   };
   float2 hnext = both(0.f);
@@ -113,7 +113,7 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
     if (at.warp == 1) hnext = state(tt - ch.cs);
     BwdStage<TX, TG, TD>& st = sm.stage[round % kStages];
     if (n > 0 && n < kTileT && ch.tab.cu) {  // the next sequence's tokens
-      clear_rows<NARROW>(st.x, n);
+      clear_rows<SPLIT>(st.x, n);
       tc::fence_proxy_async_smem();  // the stage's next tiles come by TMA
       __syncthreads();
     }
@@ -175,7 +175,7 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
         R = fma2(a, R, sm.back[at.group(w)]);
         A = mul2(A, a);
       }
-      float2 v = carry_round<NARROW, true>(ch, k.rank, round, join4(A, R), sm.carry, folds, &carry,
+      float2 v = carry_round<SPLIT, true>(ch, k.rank, round, join4(A, R), sm.carry, folds, &carry,
                                            &lost);
 #pragma unroll 4
       for (int w = 7; w >= 0; --w) {
@@ -253,13 +253,13 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
       load(round + 1);
     }
   }
-  if (k.rank == 0 && at.warp == 0 && at.half == 0) write2(p.dh0, k.row, c, p.D, carry);
+  if (k.rank == 0 && at.warp == 0 && at.part == 0) write2(p.dh0, k.row, c, p.D, carry);
   if (!GIVEN) {
     sm.sums[threadIdx.x] = join4(mul2(sA, both(kLn2)), sb);
     __syncthreads();
-    if (at.warp == 0 && at.half == 0) {
+    if (at.warp == 0 && at.part == 0) {
       float2 vA = both(0.f), vb = both(0.f);
-      for (int i = at.cl; i < kLinrecThreads; i += Shape<NARROW>::kLanes) {
+      for (int i = at.cl; i < kLinrecThreads; i += Shape<SPLIT>::kLanes) {
         const float4 q = sm.sums[i];
         vA = add2(vA, first2(q));
         vb = add2(vb, last2(q));
@@ -313,32 +313,31 @@ struct BwdRun {
   cudaError_t run() const {
     using TD = typename Wide<TX, WIDE>::type;
     using TDG = typename Wide<TD, GIVEN>::type;
-    static KernelSlots known, known_narrow;
-    const auto kernel = linrec_bwd_kernel<TX, TG, GIVEN, SCALE, TD, TDG, false>;
-    const std::atomic<int>* slots = nullptr;
-    cudaError_t e = kernel_slots(kernel, sizeof(BwdSmem<TX, TG, TD>), &known, &slots);
+    static KernelSlots known[3];
+    const auto k1 = linrec_bwd_kernel<TX, TG, GIVEN, SCALE, TD, TDG, 1>;
+    const auto k2 = linrec_bwd_kernel<TX, TG, GIVEN, SCALE, TD, TDG, 2>;
+    const auto k4 = linrec_bwd_kernel<TX, TG, GIVEN, SCALE, TD, TDG, 4>;
+    Split sp;
+    constexpr size_t smem = sizeof(BwdSmem<TX, TG, TD>);
+    cudaError_t e = choose_split(p, k1, k2, k4, smem, smem, known, &sp);
     if (e != cudaSuccess) return e;
-    return narrow_tiles(p, slots[0].load(std::memory_order_relaxed))
-               ? launch<TX, TG, GIVEN, TD, TDG, true>(
-                     linrec_bwd_kernel<TX, TG, GIVEN, SCALE, TD, TDG, true>, &known_narrow)
-               : launch<TX, TG, GIVEN, TD, TDG, false>(kernel, &known);
+    return sp.split == 4   ? launch<TX, TG, GIVEN, TD, TDG, 4>(k4, sp.cs)
+           : sp.split == 2 ? launch<TX, TG, GIVEN, TD, TDG, 2>(k2, sp.cs)
+                           : launch<TX, TG, GIVEN, TD, TDG, 1>(k1, sp.cs);
   }
-  template <typename TX, typename TG, bool GIVEN, typename TD, typename TDG, bool NARROW,
-            typename K>
-  cudaError_t launch(K kernel, KernelSlots* known) const {
+  template <typename TX, typename TG, bool GIVEN, typename TD, typename TDG, int SPLIT, typename K>
+  cudaError_t launch(K kernel, int cs) const {
     LinrecMaps maps;
     Chains c = ch;
-    c.tma = map_tiles<NARROW, TX>(&maps.x, p, p.x, p.ldx) &&
-            map_tiles<NARROW, TG>(&maps.a, p, p.a, p.lda) &&
-            (!p.b || map_tiles<NARROW, TG>(&maps.b, p, p.b, p.ldb)) &&
-            map_tiles<NARROW, TD>(&maps.dh, p, p.dh, p.lddh);
-    // one block a channel: no sums to join
-    const bool alone = p.B == 1 && most_blocks(p, Shape<NARROW>::kT) == 1;
+    c.tma = map_tiles<SPLIT, TX>(&maps.x, p, p.x, p.ldx) &&
+            map_tiles<SPLIT, TG>(&maps.a, p, p.a, p.lda) &&
+            (!p.b || map_tiles<SPLIT, TG>(&maps.b, p, p.b, p.ldb)) &&
+            map_tiles<SPLIT, TD>(&maps.dh, p, p.dh, p.lddh);
+    const bool alone = p.B == 1 && cs == 1;  // one block a channel: no sums to join
     const int vec = pairs(p.dx, p.lddx, sizeof(TD)) && pairs(p.da, p.ldda, sizeof(TDG)) &&
                     pairs(p.db, p.lddb, sizeof(TDG));
-    int cs = 1;
-    cudaError_t e = launch_chains<NARROW>(kernel, sizeof(BwdSmem<TX, TG, TD>), p, c, known, vec,
-                                          &cs, s, maps, states, alone ? nullptr : sums);
+    cudaError_t e = launch_chains<SPLIT>(kernel, sizeof(BwdSmem<TX, TG, TD>), p, c, cs, vec, s,
+                                         maps, states, alone ? nullptr : sums);
     if (e != cudaSuccess || GIVEN || alone) return e;
     linrec_sums_kernel<<<(p.D + 31) / 32, dim3(32, kSumRows), 0, s>>>(
         sums, (long long)p.B * cs, p.D, p.dA_log, p.ddt_bias);
@@ -361,7 +360,7 @@ size_t linrec_bwd_workspace_bytes(const long long* cu, int B, int T, int D, bool
   return (cu ? seq_table_bytes(B) : 0) + (states_given ? 0 : states_bytes(a)) +
          (flags & GDN_GATES_PRECOMPUTED
               ? 0
-              : align256((size_t)B * most_blocks(a, kLinrecChunk) * D * sizeof(float2)));
+              : align256((size_t)B * most_blocks(a) * D * sizeof(float2)));
 }
 
 cudaError_t launch_linrec_bwd(const LinrecArgs& a, void* workspace, cudaStream_t s) {

@@ -21,7 +21,7 @@ cudaError_t launch_linrec_scan(const LinrecArgs& a, const Chains& ch, int wide_f
                                cudaStream_t s);
 
 // The map of a tensor's tiles, where its rows start on 16 bytes.
-template <bool NARROW, typename T>
+template <int SPLIT, typename T>
 bool map_tiles(CUtensorMap* m, const LinrecArgs& p, const void* base, long long ld) {
   if (((reinterpret_cast<uintptr_t>(base) | (uintptr_t)(ld * (long long)sizeof(T))) & 15) != 0)
     return false;
@@ -30,7 +30,7 @@ bool map_tiles(CUtensorMap* m, const LinrecArgs& p, const void* base, long long 
   const cuuint64_t rows = p.cu ? 1 : p.B;
   const cuuint64_t dims[3] = {(cuuint64_t)p.D, (cuuint64_t)p.T, rows};
   const cuuint64_t strides[2] = {(cuuint64_t)ld * sizeof(T), (cuuint64_t)p.T * ld * sizeof(T)};
-  const cuuint32_t box[3] = {Shape<NARROW>::kC, Shape<NARROW>::kT, 1}, es[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {Shape<SPLIT>::kC, Shape<SPLIT>::kT, 1}, es[3] = {1, 1, 1};
   return enc(m, sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
              3, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -49,44 +49,31 @@ inline long long longest(const LinrecArgs& p) {
   return n;
 }
 // The most blocks that one chain can use.
-inline int most_blocks(const LinrecArgs& p, int tile_tokens) {
-  const long long n = longest(p);
-  int cs = 1;
-  while (cs < kMaxCluster && (long long)cs * tile_tokens < n) cs *= 2;
-  return cs;
-}
-// What the runtime says of one kernel on one device, asked once: the clusters of 1, 2, 4, 8
-// and 16 blocks that run at once (at[0]: 0 until asked).
-struct KernelSlots {
-  std::atomic<int> at[64][5];
-};
-// Blocks of a cluster (as a power of two): as many as still let every cluster of the launch
-// run at once.
-inline int cluster_size(const LinrecArgs& p, int tile_tokens, long long chains,
-                        const std::atomic<int>* slots) {
-  const int most = most_blocks(p, tile_tokens);
-  int cs = 1;
-  for (int j = 1; j < 5 && cs < most; ++j)
-    if (chains <= slots[j].load(std::memory_order_relaxed) && (1 << j) <= most) cs = 1 << j;
-  return cs;
-}
-// Whether the tiles are narrow: where the chains of 64 channels do not fill the machine and
-// a sequence is longer than a chunk.
-inline bool narrow_tiles(const LinrecArgs& p, int slots) {
-  return (long long)p.B * ((p.D + 63) / 64) < slots && longest(p) > kLinrecChunk;
+inline int most_blocks(const LinrecArgs& p) {
+  const long long n = (longest(p) + kLinrecChunk - 1) / kLinrecChunk;
+  return n < 1 ? 1 : n < kMaxCluster ? (int)n : kMaxCluster;
 }
 
+// What the runtime says of one kernel on one device, asked once: at[cs] clusters of cs blocks
+// run at once (at[1]: 0 until asked).
+struct KernelSlots {
+  std::atomic<int> at[64][kMaxCluster + 1];
+};
+// smem: of the call; most_smem: the most that any call of the kernel takes (its limit is set to
+// that once and for all), both without the cluster's folds.
 template <typename K>
-cudaError_t kernel_slots(K kernel, size_t smem, KernelSlots* known, const std::atomic<int>** slots) {
-  int dev = 0, sms = 0, per = 0;
+cudaError_t kernel_slots(K kernel, size_t smem, size_t most_smem, KernelSlots* known,
+                         const std::atomic<int>** slots) {
+  int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   std::atomic<int>* at = known->at[dev];
   *slots = at;
-  if (at[0].load(std::memory_order_acquire) != 0) return cudaSuccess;
+  if (at[1].load(std::memory_order_acquire) != 0) return cudaSuccess;
+  int sms = 0, per = 0;
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const size_t most = smem + 2 * kMaxCluster * sizeof(FoldRow);
+  const size_t most = most_smem + 2 * kMaxCluster * sizeof(FoldRow);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
   if (e == cudaSuccess)
@@ -94,8 +81,7 @@ cudaError_t kernel_slots(K kernel, size_t smem, KernelSlots* known, const std::a
   if (e == cudaSuccess)
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kLinrecThreads, smem);
   if (e != cudaSuccess) return e;
-  for (int j = 1; j < 5; ++j) {
-    const int cs = 1 << j;
+  for (int cs = 2; cs <= kMaxCluster; ++cs) {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)cs;
@@ -110,36 +96,64 @@ cudaError_t kernel_slots(K kernel, size_t smem, KernelSlots* known, const std::a
     int n = 0;
     e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
     if (e != cudaSuccess) return e;
-    at[j].store(n, std::memory_order_relaxed);
+    at[cs].store(n, std::memory_order_relaxed);
   }
-  at[0].store(sms * (per > 0 ? per : 1), std::memory_order_release);
+  at[1].store(sms * (per > 0 ? per : 1), std::memory_order_release);
   return cudaSuccess;
 }
 
-template <bool NARROW, typename K, typename... More>
-cudaError_t launch_chains(K kernel, size_t smem, const LinrecArgs& p, const Chains& chains,
-                          KernelSlots* known, int vec, int* cluster, cudaStream_t s,
-                          More... more) {
-  const std::atomic<int>* slots = nullptr;
-  cudaError_t e = kernel_slots(kernel, smem, known, &slots);
-  if (e != cudaSuccess) return e;
+// How a call is cut: chunks of a tile, blocks of a cluster.
+struct Split {
+  int split, cs;
+};
+inline long long chains_of(const LinrecArgs& p, int split) {
+  return (long long)p.B * ((p.D * (long long)split + 63) / 64);
+}
+// The one of the three shapes that has the most blocks at work at once: whole chunks of 64
+// channels where those chains fill the machine; else the largest cluster whose launch still
+// runs at once, the smaller cluster (fewer exchanges) where shapes are equal.
+template <typename K>
+cudaError_t choose_split(const LinrecArgs& p, K k1, K k2, K k4, size_t smem, size_t most_smem,
+                         KernelSlots* known, Split* out) {
+  *out = Split{1, 1};
+  const long long chunks = (longest(p) + kLinrecChunk - 1) / kLinrecChunk;
+  long long best = 0;
+  for (int j = 0; j < 3; ++j) {
+    const int split = 1 << j;
+    const std::atomic<int>* slots = nullptr;
+    cudaError_t e = kernel_slots(j == 0 ? k1 : j == 1 ? k2 : k4, smem, most_smem, known + j, &slots);
+    if (e != cudaSuccess) return e;
+    const long long n = chains_of(p, split), tiles = (chunks + split - 1) / split;
+    if (n > slots[1].load(std::memory_order_relaxed) || (j > 0 && chunks < split)) break;
+    int cs = 1;
+    for (int i = 2; i <= kMaxCluster && i <= tiles; ++i)
+      if (n <= slots[i].load(std::memory_order_relaxed)) cs = i;
+    if (n * cs > best || (n * cs == best && cs < out->cs)) {
+      best = n * cs;
+      *out = Split{split, cs};
+    }
+  }
+  return cudaSuccess;
+}
+
+template <int SPLIT, typename K, typename... More>
+cudaError_t launch_chains(K kernel, size_t smem, const LinrecArgs& p, const Chains& chains, int cs,
+                          int vec, cudaStream_t s, More... more) {
   Chains ch = chains;
-  ch.nblk = (p.D + Shape<NARROW>::kC - 1) / Shape<NARROW>::kC;
-  const long long n = (long long)p.B * ch.nblk;
-  ch.cs = cluster_size(p, Shape<NARROW>::kT, n, slots);
-  *cluster = ch.cs;
+  ch.cs = cs;
+  ch.nblk = (p.D + Shape<SPLIT>::kC - 1) / Shape<SPLIT>::kC;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)ch.cs;
+  attr[0].val.clusterDim.x = (unsigned)cs;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(n * ch.cs));
+  cfg.gridDim = dim3((unsigned)((long long)p.B * ch.nblk * cs));
   cfg.blockDim = dim3(kLinrecThreads);
-  cfg.dynamicSmemBytes = smem + (ch.cs > 1 || NARROW ? 2 * ch.cs * sizeof(FoldRow) : 0);
+  cfg.dynamicSmemBytes = smem + (cs > 1 || SPLIT > 1 ? 2 * cs * sizeof(FoldRow) : 0);
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = ch.cs > 1 ? 1 : 0;
+  cfg.numAttrs = cs > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, p, ch, vec, more...);
 }
 

@@ -29,33 +29,33 @@ constexpr int kMaxCluster = 16;
 constexpr int kGroup = 4;   // tokens whose gates are formed together
 constexpr int kTile = 64 * 64;  // elements of a tile
 
-// A tile's shape: one chunk of 64 channels, or two chunks of 32 where there are few chains to
-// share the machine (half the channels are twice the chains, and half the rounds of the
-// cluster; its rows are 64 bytes of bf16 instead of 128).
-template <bool NARROW>
+// A tile's shape: one chunk of 64 channels, or 2 of 32 or 4 of 16 where there are few chains
+// to share the machine (half the channels are twice the chains and half the rounds of a
+// cluster; their rows are 64 or 32 bytes of bf16 instead of 128).
+template <int SPLIT>
 struct Shape {
-  static constexpr int kChunks = NARROW ? 2 : 1;
-  static constexpr int kT = kChunks * kLinrecChunk, kC = 64 / kChunks;
+  static constexpr int kChunks = SPLIT;
+  static constexpr int kT = SPLIT * kLinrecChunk, kC = 64 / SPLIT;
   static constexpr int kLanes = kC / 2;  // of one group of tokens
 };
 // A thread's place in it.
-template <bool NARROW>
+template <int SPLIT>
 struct Spot {
-  int lane, warp, cl, half, first;  // channel pair, the warp's lower or upper lanes, first token
+  int lane, warp, cl, part, first;  // channel pair, which of the warp's groups, first token
   __device__ __forceinline__ Spot() {
-    constexpr int kLanes = Shape<NARROW>::kLanes;
+    constexpr int kLanes = Shape<SPLIT>::kLanes;
     lane = threadIdx.x & 31;
     warp = threadIdx.x / 32;
     cl = lane % kLanes;
-    half = lane / kLanes;
+    part = lane / kLanes;
     first = (threadIdx.x / kLanes) * kPer;
   }
   // first element of the thread in a tile
-  __device__ __forceinline__ int mine() const { return first * Shape<NARROW>::kC + 2 * cl; }
-  // For the joining warps, whose upper lanes (NARROW) take the second chunk: where group w of
+  __device__ __forceinline__ int mine() const { return first * Shape<SPLIT>::kC + 2 * cl; }
+  // For the joining warps, each part of which takes one of the tile's chunks: where group w of
   // the lane's chunk has its fold.
   __device__ __forceinline__ int group(int w) const {
-    return (half * 8 + w) * Shape<NARROW>::kLanes + cl;
+    return (part * 8 + w) * Shape<SPLIT>::kLanes + cl;
   }
 };
 
@@ -89,13 +89,13 @@ struct Chain {
   int row, c0;     // sequence, first channel
   int chunks, tiles, rank;
 };
-template <bool NARROW>
+template <int SPLIT>
 __device__ __forceinline__ Chain chain_of(const LinrecArgs& p, const Chains& ch) {
   Chain k;
   const int id = blockIdx.x / ch.cs;
   k.rank = blockIdx.x % ch.cs;
   k.row = id / ch.nblk;
-  k.c0 = (id - k.row * ch.nblk) * Shape<NARROW>::kC;
+  k.c0 = (id - k.row * ch.nblk) * Shape<SPLIT>::kC;
   if (ch.tab.cu == nullptr) {
     k.tok = (long long)k.row * p.T;
     k.len = p.T;
@@ -106,7 +106,7 @@ __device__ __forceinline__ Chain chain_of(const LinrecArgs& p, const Chains& ch)
     k.chunk0 = ch.tab.chunk0[k.row];
   }
   k.chunks = (int)((k.len + kLinrecChunk - 1) / kLinrecChunk);
-  k.tiles = (k.chunks + Shape<NARROW>::kChunks - 1) / Shape<NARROW>::kChunks;
+  k.tiles = (k.chunks + Shape<SPLIT>::kChunks - 1) / Shape<SPLIT>::kChunks;
   return k;
 }
 
@@ -136,8 +136,8 @@ __device__ __forceinline__ void st_async_peer(uint32_t addr, float4 v, uint32_t 
 
 // One round of the carry, by one warp: own is the (A, H) of the lane's chunk of this block's
 // tile.  Returns what enters that chunk and moves `carry` behind the round's last chunk; BACK:
-// a tile's second chunk comes first.  `lost`: a wait has expired, later ones are not tried.
-template <bool NARROW, bool BACK>
+// a tile's last chunk comes first.  `lost`: a wait has expired, later ones are not tried.
+template <int SPLIT, bool BACK>
 __device__ __forceinline__ float2 carry_round(const Chains& ch, int rank, int round, float4 own,
                                               CarrySmem& sm, FoldRow* folds, float2* carry,
                                               bool* lost) {
@@ -155,28 +155,23 @@ __device__ __forceinline__ float2 carry_round(const Chains& ch, int rank, int ro
       *lost = !__all_sync(0xffffffffu, ok);
       if (*lost && lane == 0) report_timeout(ch.status, 0x4c52);
     }
-  } else if (NARROW) {  // the lanes' two chunks
+  } else if (SPLIT > 1) {  // the parts' chunks
     row[0][lane] = own;
     __syncwarp();
   }
   float2 in = *carry, v = *carry;
-  if (!NARROW && ch.cs == 1) {
+  if (SPLIT == 1 && ch.cs == 1) {
     *carry = fma2(first2(own), in, last2(own));
     return in;
   }
-  const int half = lane / 16, cl = lane % 16;
+  constexpr int kLanes = Shape<SPLIT>::kLanes;
+  const int part = lane / kLanes, cl = lane % kLanes;
   for (int r = 0; r < ch.cs; ++r) {
-    if (NARROW) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int h = BACK ? 1 - i : i;
-        if (r == rank && h == half) in = v;
-        const float4 f = row[r][16 * h + cl];
-        v = fma2(first2(f), v, last2(f));
-      }
-    } else {
-      if (r == rank) in = v;
-      const float4 f = row[r][lane];
+    for (int i = 0; i < SPLIT; ++i) {
+      const int h = BACK ? SPLIT - 1 - i : i;
+      if (r == rank && h == part) in = v;
+      const float4 f = row[r][kLanes * h + cl];
       v = fma2(first2(f), v, last2(f));
     }
   }
@@ -226,10 +221,10 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-template <bool NARROW, typename T>
+template <int SPLIT, typename T>
 __device__ __forceinline__ void load_elements(T* dst, const void* base, long long ld,
                                               long long tok, int n, int c0, int D) {
-  constexpr int kTileC = Shape<NARROW>::kC, kTileT = Shape<NARROW>::kT;
+  constexpr int kTileC = Shape<SPLIT>::kC, kTileT = Shape<SPLIT>::kT;
   constexpr int kStep = kLinrecThreads / kTileC;  // rows at once
   const int r0 = threadIdx.x / kTileC, c = threadIdx.x % kTileC;
   const bool in = c < D - c0;
@@ -246,9 +241,9 @@ __device__ __forceinline__ void load_elements(T* dst, const void* base, long lon
   }
 }
 // Clears the rows of a tile behind its n tokens.
-template <bool NARROW, typename T>
+template <int SPLIT, typename T>
 __device__ __forceinline__ void clear_rows(T* tile, int n) {
-  for (int i = n * Shape<NARROW>::kC + threadIdx.x; i < kTile; i += kLinrecThreads)
+  for (int i = n * Shape<SPLIT>::kC + threadIdx.x; i < kTile; i += kLinrecThreads)
     tile[i] = from_f32<T>(0.f);
 }
 
@@ -269,7 +264,7 @@ __device__ __forceinline__ void put2(T* p, float2 v, int cols) {
   if (cols > 1) p[1] = from_f32<T>(v.y);
 }
 // An output tensor of a block: a 64-bit base that moves from tile to tile, the same for all
-// threads, and 32-bit byte offsets inside a tile (128 rows of at most 2^22 elements).
+// threads, and 32-bit byte offsets inside a tile (256 rows of at most 2^21 elements).
 template <typename T>
 struct Rows {
   char* base;
