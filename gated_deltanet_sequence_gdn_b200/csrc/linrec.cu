@@ -218,29 +218,49 @@ __global__ void __launch_bounds__(128) linrec_step_kernel(LinrecArgs p, float* s
 constexpr int kPiece = 240;  // entries of a table piece passed by value (< 4 KB of arguments)
 struct TabPiece {
   long long cu[kPiece];
-  int chunk0[kPiece];
+  int chunk0[kPiece], order[kPiece];
   int first, n;
 };
-__global__ void seq_table_kernel(TabPiece p, long long* cu, int* chunk0) {
+__global__ void seq_table_kernel(TabPiece p, long long* cu, int* chunk0, int* order) {
   for (int i = threadIdx.x; i < p.n; i += blockDim.x) {
     cu[p.first + i] = p.cu[i];
     chunk0[p.first + i] = p.chunk0[i];
+    order[p.first + i] = p.order[i];
   }
 }
-cudaError_t fill_seq_table(const long long* cu, int B, const SeqTab& tab, cudaStream_t s) {
+// The sequences' order: by eighths of the longest one's length, from the last to the first,
+// each in the order of the batch.
+struct Order {
+  const long long* cu;
+  int B, eighth, next;
+  long long most;
+  int take() {
+    for (; eighth >= 0; --eighth, next = 0)
+      while (next < B) {
+        const int i = next++;
+        const long long e = (cu[i + 1] - cu[i]) * 8 / most;
+        if ((e < 7 ? e : 7) == eighth) return i;
+      }
+    return 0;  // entry B, which is not a sequence
+  }
+};
+cudaError_t fill_seq_table(const LinrecArgs& a, const SeqTab& tab, cudaStream_t s) {
+  const long long most = longest(a);
+  Order order{a.cu, a.B, 7, 0, most > 0 ? most : 1};
   long long chunks = 0;
   TabPiece p;
-  for (int i0 = 0; i0 <= B; i0 += kPiece) {
+  for (int i0 = 0; i0 <= a.B; i0 += kPiece) {
     p.first = i0;
-    p.n = B + 1 - i0 < kPiece ? B + 1 - i0 : kPiece;
+    p.n = a.B + 1 - i0 < kPiece ? a.B + 1 - i0 : kPiece;
     for (int i = 0; i < p.n; ++i) {
       const int j = i0 + i;
-      p.cu[i] = cu[j];
+      p.cu[i] = a.cu[j];
       p.chunk0[i] = (int)chunks;
-      if (j < B) chunks += (cu[j + 1] - cu[j] + kLinrecChunk - 1) / kLinrecChunk;
+      p.order[i] = order.take();
+      if (j < a.B) chunks += (a.cu[j + 1] - a.cu[j] + kLinrecChunk - 1) / kLinrecChunk;
     }
     seq_table_kernel<<<1, 256, 0, s>>>(p, const_cast<long long*>(tab.cu),
-                                       const_cast<int*>(tab.chunk0));
+                                       const_cast<int*>(tab.chunk0), const_cast<int*>(tab.order));
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
@@ -298,17 +318,16 @@ size_t linrec_workspace_bytes(const long long* cu, int B, int T, int D) {
   return cu ? seq_table_bytes(B) : 0;
 }
 
-cudaError_t make_chains(const LinrecArgs& a, void* workspace, bool table, cudaStream_t s,
-                        Chains* ch) {
+cudaError_t make_chains(const LinrecArgs& a, void* workspace, cudaStream_t s, Chains* ch) {
   if (a.cu) {
     char* ws = static_cast<char*>(workspace);
     ch->tab.cu = reinterpret_cast<const long long*>(ws);
-    ch->tab.chunk0 =
-        reinterpret_cast<const int*>(ws + align256((size_t)(a.B + 1) * sizeof(long long)));
-    if (table) {
-      cudaError_t e = fill_seq_table(a.cu, a.B, ch->tab, s);
-      if (e != cudaSuccess) return e;
-    }
+    ws += align256((size_t)(a.B + 1) * sizeof(long long));
+    ch->tab.chunk0 = reinterpret_cast<const int*>(ws);
+    ws += align256((size_t)(a.B + 1) * sizeof(int));
+    ch->tab.order = reinterpret_cast<const int*>(ws);
+    cudaError_t e = fill_seq_table(a, ch->tab, s);
+    if (e != cudaSuccess) return e;
   }
   ch->status = status_word();
   if (ch->status == nullptr) return cudaErrorUnknown;
@@ -326,7 +345,7 @@ cudaError_t launch_linrec_scan(const LinrecArgs& a, const Chains& ch, int wide_f
 
 cudaError_t launch_linrec_fwd(const LinrecArgs& a, void* workspace, cudaStream_t s) {
   Chains ch{};
-  cudaError_t e = make_chains(a, workspace, true, s, &ch);
+  cudaError_t e = make_chains(a, workspace, s, &ch);
   return e != cudaSuccess ? e : launch_linrec_scan(a, ch, GDN_OUT_F32, s);
 }
 

@@ -366,7 +366,7 @@ size_t linrec_bwd_workspace_bytes(const long long* cu, int B, int T, int D, bool
 cudaError_t launch_linrec_bwd(const LinrecArgs& a, void* workspace, cudaStream_t s) {
   char* ws = static_cast<char*>(workspace);
   Chains ch{};
-  cudaError_t e = make_chains(a, ws, true, s, &ch);
+  cudaError_t e = make_chains(a, ws, s, &ch);
   if (e != cudaSuccess) return e;
   if (a.cu) ws += seq_table_bytes(a.B);
   const float* states = a.states;

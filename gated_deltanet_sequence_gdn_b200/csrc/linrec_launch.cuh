@@ -10,12 +10,12 @@ namespace gdn {
 
 inline size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 inline size_t seq_table_bytes(int B) {
-  return align256((size_t)(B + 1) * sizeof(long long)) + align256((size_t)(B + 1) * sizeof(int));
+  return align256((size_t)(B + 1) * sizeof(long long)) +
+         2 * align256((size_t)(B + 1) * sizeof(int));
 }
 
-// Fills in what every launch of a call shares; `table`: writes the table of a packed batch.
-cudaError_t make_chains(const LinrecArgs& a, void* workspace, bool table, cudaStream_t s,
-                        Chains* ch);
+// Fills in what every launch of a call shares and writes the table of a packed batch.
+cudaError_t make_chains(const LinrecArgs& a, void* workspace, cudaStream_t s, Chains* ch);
 // The forward scan; wide_flag: the call's flag for float32 outputs.
 cudaError_t launch_linrec_scan(const LinrecArgs& a, const Chains& ch, int wide_flag,
                                cudaStream_t s);

@@ -63,6 +63,7 @@ struct Spot {
 struct SeqTab {
   const long long* cu;  // NULL: dense rows
   const int* chunk0;
+  const int* order;     // the sequences, long ones first (they would else end the launch alone)
 };
 
 // Maps of the inputs' tiles.
@@ -96,6 +97,7 @@ __device__ __forceinline__ Chain chain_of(const LinrecArgs& p, const Chains& ch)
   k.rank = blockIdx.x % ch.cs;
   k.row = id / ch.nblk;
   k.c0 = (id - k.row * ch.nblk) * Shape<SPLIT>::kC;
+  if (ch.tab.cu != nullptr) k.row = ch.tab.order[k.row];
   if (ch.tab.cu == nullptr) {
     k.tok = (long long)k.row * p.T;
     k.len = p.T;
