@@ -665,13 +665,20 @@ def _here(dev):
     return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
+def _new(t, dtype):
+    """A contiguous tensor of t's shape (the call that does it in the least host time)."""
+    if t.dtype is dtype and t.is_contiguous():
+        return torch.empty_like(t)
+    return t.new_empty(t.shape, dtype=dtype)
+
+
 def _like(t, dtype, shape, dev, name):
     """Raises unless the tensor has this dtype, shape and device."""
     if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != dev:
+    if t.get_device() != dev.index:
         raise ValueError(f"{name}: on {t.device}, expected {dev}")
 
 
@@ -805,10 +812,10 @@ def gdn_linrec_fwd(x, a, b=None, A_log=None, dt_bias=None, h0=None, *, cu_seqlen
     dev, f32 = x.device, torch.float32
     odt = f32 if out_f32 else x.dtype
     if h is None:
-        h = x.new_empty(x.shape, dtype=odt)
+        h = _new(x, odt)
     ph, ldh = _strided(h, odt, x.shape, dev, "h")
     if ht is None and want_ht:
-        ht = x.new_empty((B, D), dtype=f32)
+        ht = x.new_empty((B, D), dtype=f32) if h0 is None else torch.empty_like(h0)
     if want_states or states is not None:
         shape = (gdn_linrec_chunks(B, T, cu), D)
         if states is None:
@@ -843,13 +850,11 @@ def gdn_linrec_bwd(x, a, b, A_log, dt_bias, h0, dh, dht=None, *, cu_seqlens=None
     ddt = f32 if grad_f32 else x.dtype
     gdt = f32 if gates_precomputed else ddt
     pdh, lddh = _strided(dh, ddt, x.shape, dev, "dh")
-    out = {"dx": x.new_empty(x.shape, dtype=ddt), "da": x.new_empty(x.shape, dtype=gdt),
-           "db": None if b is None else x.new_empty(x.shape, dtype=gdt),
+    out = {"dx": _new(x, ddt), "da": _new(x, gdt), "db": None if b is None else _new(x, gdt),
            "dA_log": None, "ddt_bias": None,
            "dh0": x.new_empty((B, D), dtype=f32) if want_dh0 else None}
     if not gates_precomputed:
-        out["dA_log"] = x.new_empty((D,), dtype=f32)
-        out["ddt_bias"] = x.new_empty((D,), dtype=f32)
+        out["dA_log"], out["ddt_bias"] = torch.empty_like(A_log), torch.empty_like(dt_bias)
     ps = None
     if states is not None:
         ps = _dense(states, f32, (gdn_linrec_chunks(B, T, cu), D), dev, "states")
@@ -877,7 +882,7 @@ def gdn_linrec_step(x, a, b, A_log, dt_bias, state, *, input_scale="none",
     ins, lds, flags = _linrec_inputs(x, a, b, A_log, dt_bias, gates_precomputed, input_scale)
     odt = torch.float32 if out_f32 else x.dtype
     if h is None:
-        h = x.new_empty((N, D), dtype=odt)
+        h = _new(x, odt)
     ph, ldh = _strided(h, odt, (N, D), x.device, "h")
     _check(lib.gdn_linrec_step(*ins, _dense(state, torch.float32, (N, D), x.device, "state"), N,
                                D, *lds, _dtype_code(x.dtype), flags | (OUT_F32 if out_f32 else 0),
@@ -930,9 +935,9 @@ def _rope_fwd(_, q, k, positions, inv_freq, q_weight, k_weight, norm, eps, scale
     args, flags, dt, dev, lead = _rope_inputs(q, k, positions, inv_freq, q_weight, k_weight,
                                               norm, interleaved)
     if q is not None and q_out is None:
-        q_out = q.new_empty(q.shape)
+        q_out = _new(q, dt)
     if k is not None and k_out is None:
-        k_out = k.new_empty(k.shape)
+        k_out = _new(k, dt)
     po = _strided(q_out, dt, () if q is None else q.shape, dev, "q_out", 2)
     ko = _strided(k_out, dt, () if k is None else k.shape, dev, "k_out", 2)
     _check(lib.gdn_qk_norm_rope(*args, _dtype_code(dt), flags, eps, scale, *po, *ko,
@@ -965,8 +970,7 @@ def _rope_bwd(_, q, k, positions, inv_freq, q_weight, k_weight, dq_out, dk_out, 
     gdt = torch.float32 if grad_f32 else dt
     gq = _strided(dq_out, gdt, () if q is None else q.shape, dev, "dq_out", 2)
     gk = _strided(dk_out, gdt, () if k is None else k.shape, dev, "dk_out", 2)
-    out = {"dq": None if q is None else q.new_empty(q.shape, dtype=gdt),
-           "dk": None if k is None else k.new_empty(k.shape, dtype=gdt)}
+    out = {"dq": None if q is None else _new(q, gdt), "dk": None if k is None else _new(k, gdt)}
     for name, w in (("dq_weight", q_weight), ("dk_weight", k_weight)):
         out[name] = None if w is None else torch.empty_like(w)
     need = 0
