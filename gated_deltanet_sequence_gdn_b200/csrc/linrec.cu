@@ -182,37 +182,77 @@ linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
   carry_end(ch);
 }
 
-// Two channels from anywhere a row has them.
-template <typename T>
-__device__ __forceinline__ float2 take2(const void* base, long long at, int cols) {
+// The step: HBM-bound on the float32 state, read and written once.  A thread takes 4 channels
+// of one sequence, in pieces of 4 elements (VEC: the rows are aligned to them) or one by one.
+template <bool VEC, typename T>
+__device__ __forceinline__ void take4(const void* base, long long at, int cols, float2* f) {
   const T* p = static_cast<const T*>(base) + at;
-  return make_float2(to_f32(p[0]), cols > 1 ? to_f32(p[1]) : 0.f);
+  if (!VEC) {
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = i < cols ? to_f32(p[i]) : 0.f;
+    f[0] = make_float2(v[0], v[1]);
+    f[1] = make_float2(v[2], v[3]);
+  } else if (sizeof(T) == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    f[0] = make_float2(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u));
+    f[1] = make_float2(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
+  } else {
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    f[0] = make_float2(v.x, v.y);
+    f[1] = make_float2(v.z, v.w);
+  }
 }
-template <typename TX, typename TG, bool GIVEN, int SCALE, typename TO>
-__global__ void __launch_bounds__(128) linrec_step_kernel(LinrecArgs p, float* state) {
-  const int blocks = (p.D + 255) / 256;
+template <bool VEC, typename T>
+__device__ __forceinline__ void leave4(void* base, long long at, int cols, const float2* f) {
+  T* p = static_cast<T*>(base) + at;
+  if (!VEC) {
+    const float v[4] = {f[0].x, f[0].y, f[1].x, f[1].y};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < cols) p[i] = from_f32<T>(v[i]);
+  } else if (sizeof(T) == 2) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(f[0].x, f[0].y);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(f[1].x, f[1].y);
+    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
+                                              *reinterpret_cast<const uint32_t*>(&b));
+  } else {
+    *reinterpret_cast<float4*>(p) = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+  }
+}
+constexpr int kStepThreads = 128;
+template <typename TX, typename TG, bool GIVEN, int SCALE, typename TO, bool VEC>
+__global__ void __launch_bounds__(kStepThreads) linrec_step_kernel(LinrecArgs p, float* state) {
+  const int blocks = (p.D + 4 * kStepThreads - 1) / (4 * kStepThreads);
   const long long r = blockIdx.x / blocks;
-  const int c = (blockIdx.x % blocks) * 256 + 2 * threadIdx.x, cols = p.D - c;
+  const int c = (blockIdx.x % blocks) * 4 * kStepThreads + 4 * threadIdx.x, cols = p.D - c;
   if (cols <= 0) return;
-  GateConst gc{both(0.f), both(0.f)};
-  if (!GIVEN) gc = gate_const(p.A_log, p.dt_bias, c, p.D);
-  float2 e = take2<TG>(p.a, r * p.lda + c, cols);
-  decay_exponents<GIVEN, 1>(&e, gc);
-  const float2 al = ex2_2(e);
-  float2 u = take2<TX>(p.x, r * p.ldx + c, cols);
+  float2 e[2], x[2], b[2], st[2], al[2], f[2];
+  take4<VEC, TG>(p.a, r * p.lda + c, cols, e);
+  take4<VEC, TX>(p.x, r * p.ldx + c, cols, x);
+  take4<VEC, float>(state, r * p.D + c, cols, st);
+  if (p.b) take4<VEC, TG>(p.b, r * p.ldb + c, cols, b);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    GateConst gc{both(0.f), both(0.f)};
+    if (!GIVEN) gc = gate_const(p.A_log, p.dt_bias, c + 2 * i, p.D);
+    decay_exponents<GIVEN, 1>(e + i, gc);
+    al[i] = ex2_2(e[i]);
+  }
   if (SCALE != kScaleNone) {
-    float2 f;
-    input_scales<SCALE, 1>(&e, &al, &f);
-    u = mul2(u, f);
+    input_scales<SCALE, 2>(e, al, f);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) x[i] = mul2(x[i], f[i]);
   }
   if (p.b) {
-    float2 b = take2<TG>(p.b, r * p.ldb + c, cols);
-    write_gates<GIVEN, 1>(&b);
-    u = mul2(u, b);
+    write_gates<GIVEN, 2>(b);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) x[i] = mul2(x[i], b[i]);
   }
-  const float2 st = fma2(al, read2(state, r, c, p.D), u);
-  write2(state, r, c, p.D, st);
-  put2(static_cast<TO*>(p.h) + r * p.ldh + c, st, cols);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) st[i] = fma2(al[i], st[i], x[i]);
+  leave4<VEC, float>(state, r * p.D + c, cols, st);
+  leave4<VEC, TO>(p.h, r * p.ldh + c, cols, st);
 }
 
 constexpr int kPiece = 240;  // entries of a table piece passed by value (< 4 KB of arguments)
@@ -304,10 +344,23 @@ struct StepRun {
   cudaStream_t s;
   template <typename TX, typename TG, bool GIVEN, int SCALE, bool WIDE>
   cudaError_t run() const {
-    const long long blocks = (long long)p.B * ((p.D + 255) / 256);
-    linrec_step_kernel<TX, TG, GIVEN, SCALE, typename Wide<TX, WIDE>::type>
-        <<<(unsigned)blocks, 128, 0, s>>>(p, state);
+    using TO = typename Wide<TX, WIDE>::type;
+    const long long blocks =
+        (long long)p.B * ((p.D + 4 * kStepThreads - 1) / (4 * kStepThreads));
+    const bool vec = p.D % 4 == 0 && fours(p.x, p.ldx, sizeof(TX)) &&
+                     fours(p.a, p.lda, sizeof(TG)) && fours(p.b, p.ldb, sizeof(TG)) &&
+                     fours(p.h, p.ldh, sizeof(TO)) && fours(state, p.D, sizeof(float));
+    if (vec)
+      linrec_step_kernel<TX, TG, GIVEN, SCALE, TO, true>
+          <<<(unsigned)blocks, kStepThreads, 0, s>>>(p, state);
+    else
+      linrec_step_kernel<TX, TG, GIVEN, SCALE, TO, false>
+          <<<(unsigned)blocks, kStepThreads, 0, s>>>(p, state);
     return cudaGetLastError();
+  }
+  // rows whose pieces of 4 elements are aligned
+  static bool fours(const void* q, long long ld, int es) {
+    return ((reinterpret_cast<uintptr_t>(q) | (uintptr_t)(ld * es)) & (4 * es - 1)) == 0;
   }
 };
 
