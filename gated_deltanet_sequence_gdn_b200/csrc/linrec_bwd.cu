@@ -151,10 +151,16 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
           A = mul2(A, al[i0 + i]);
         }
       }
+      if (n == kTileT) {
 #pragma unroll
-      for (int i = kPer - 1; i >= 0; --i) {
-        if (first + i < n) R = add2(get2(st.dh + mine + i * kC), R);
-        R = mul2(al[i], R);
+        for (int i = kPer - 1; i >= 0; --i)
+          R = mul2(al[i], add2(get2(st.dh + mine + i * kC), R));
+      } else {
+#pragma unroll
+        for (int i = kPer - 1; i >= 0; --i) {
+          if (first + i < n) R = add2(get2(st.dh + mine + i * kC), R);
+          R = mul2(al[i], R);
+        }
       }
       sm.carry.fold[threadIdx.x] = join4(A, H);
       sm.back[threadIdx.x] = R;
@@ -204,41 +210,47 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
     }
     float2 cc = sm.back[threadIdx.x];
     float2 tA = both(0.f), tb = both(0.f);
-    const bool whole = n == kTileT && cols > 1 && vec;
-#pragma unroll
-    for (int i = kPer - 1; i >= 0; --i) {
-      if (first + i >= n) continue;
+    auto token = [&](int i, float2* dx, float2* da, float2* db) {
       const int el = mine + i * kC;
       const float2 lam = add2(get2(st.dh + el), cc);
       cc = mul2(al[i], lam);
       const float2 lx = mul2(lam, get2(st.x + el));
-      float2 dg = mul2(cc, hp[i]), dx = mul2(lam, be[i]), db = lx;
+      float2 dg = mul2(cc, hp[i]);
+      *dx = mul2(lam, be[i]);
+      *db = lx;
       if (SCALE != kScaleNone) {
         const float2 q = make_float2(input_scale_slope<SCALE>(al[i].x, f[i].x),
                                      input_scale_slope<SCALE>(al[i].y, f[i].y));
         dg = fma2(mul2(lx, be[i]), q, dg);
-        dx = mul2(dx, f[i]);
-        db = mul2(db, f[i]);
+        *dx = mul2(*dx, f[i]);
+        *db = mul2(*db, f[i]);
       }
-      float2 da = dg;
+      *da = dg;
       if (!GIVEN) {
-        if (p.b) db = mul2(mul2(db, be[i]), write_gate_rest(get2(st.b + el), be[i]));
-        da = mul2(dg, slope[i]);
-        tb = add2(tb, da);
+        if (p.b) *db = mul2(mul2(*db, be[i]), write_gate_rest(get2(st.b + el), be[i]));
+        *da = mul2(dg, slope[i]);
+        tb = add2(tb, *da);
         // dg log2(e) times e, which is -inf where alpha = 0
         tA = fma2(dg, make_float2(fmaxf(e[i].x, -3e38f), fmaxf(e[i].y, -3e38f)), tA);
       }
-      TD* px = odx.at(i);
-      TDG* pa = oda.at(i);
-      TDG* pb = odb.at(i);
-      if (whole) {
-        put2(px, dx);
-        put2(pa, da);
-        if (p.b) put2(pb, db);
-      } else {
-        put2(px, dx, cols);
-        put2(pa, da, cols);
-        if (p.b) put2(pb, db, cols);
+    };
+    float2 dx, da, db;
+    if (n == kTileT && cols > 1 && vec) {
+#pragma unroll
+      for (int i = kPer - 1; i >= 0; --i) {
+        token(i, &dx, &da, &db);
+        put2(odx.at(i), dx);
+        put2(oda.at(i), da);
+        if (p.b) put2(odb.at(i), db);
+      }
+    } else {
+#pragma unroll
+      for (int i = kPer - 1; i >= 0; --i) {
+        if (first + i >= n) continue;
+        token(i, &dx, &da, &db);
+        put2(odx.at(i), dx, cols);
+        put2(oda.at(i), da, cols);
+        if (p.b) put2(odb.at(i), db, cols);
       }
     }
     odx.advance(-step);
