@@ -648,11 +648,12 @@ def _on_device(fn):
     device's current stream); what it allocates then belongs to that stream."""
     @functools.wraps(fn)
     def call(first, *args, stream=None, **kw):
-        dev = first.device
-        if dev.type != "cuda":
+        index = first.get_device()
+        if index < 0:
             raise ValueError("tensor must live on a CUDA device")
-        if stream is None and dev.index == torch.cuda.current_device():
+        if stream is None and index == torch.cuda.current_device():
             return fn(first, *args, **kw)
+        dev = first.device
         if stream is not None and stream.device != dev:
             raise ValueError(f"stream of {stream.device} for tensors of {dev}")
         with torch.cuda.device(dev), torch.cuda.stream(stream):
@@ -702,22 +703,19 @@ def _strided(t, dtype, shape, dev, name, tail=1):
     row = shape[-1] if tail == 1 else shape[-1] * shape[-2]
     if t.is_contiguous():
         return t.data_ptr(), row
-    st, lead = t.stride(), t.dim() - tail
-    inner = 1
-    for i in range(t.dim() - 1, lead - 1, -1):
-        if shape[i] > 1 and st[i] != inner:
-            raise ValueError(f"{name}: the elements of a token must be contiguous")
-        inner *= shape[i]
-    ld = row
-    if t.numel() > 0:
-        if shape[lead - 1] > 1:
-            ld = st[lead - 1]
-            if lead == 2 and shape[0] > 1 and st[0] != ld * shape[1]:
-                raise ValueError(f"{name}: the tokens must be a fixed distance apart")
-        elif lead == 2 and shape[0] > 1:
-            ld = st[0]
-        if ld < row:
-            raise ValueError(f"{name}: tokens overlap (a broadcast view?)")
+    st = t.stride()
+    if (st[-1] != 1 and shape[-1] > 1) or (tail == 2 and st[-2] != shape[-1] and shape[-2] > 1):
+        raise ValueError(f"{name}: the elements of a token must be contiguous")
+    if len(st) == tail + 1:
+        ld = st[0] if shape[0] > 1 else row
+    elif shape[1] > 1:
+        ld = st[1]
+        if shape[0] > 1 and st[0] != ld * shape[1]:
+            raise ValueError(f"{name}: the tokens must be a fixed distance apart")
+    else:
+        ld = st[0] if shape[0] > 1 else row
+    if ld < row:
+        raise ValueError(f"{name}: tokens overlap (a broadcast view?)")
     return t.data_ptr(), ld
 
 

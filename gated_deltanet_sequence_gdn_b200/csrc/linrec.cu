@@ -177,6 +177,7 @@ linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
       }
       out.advance(step);
     }
+    if (at.warp == 0) carry_rest<SPLIT, false>(ch, k.rank, round, folds, &carry);
   }
   if (k.rank == 0 && at.warp == 0 && at.part == 0) write2(p.ht, k.row, c, p.D, carry);
   carry_end(ch);

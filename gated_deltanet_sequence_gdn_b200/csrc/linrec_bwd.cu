@@ -253,6 +253,7 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
         if (p.b) put2(odb.at(i), db, cols);
       }
     }
+    if (at.warp == 0) carry_rest<SPLIT, true>(ch, k.rank, round, folds, &carry);
     odx.advance(-step);
     oda.advance(-step);
     odb.advance(-step);

@@ -136,13 +136,40 @@ __device__ __forceinline__ void st_async_peer(uint32_t addr, float4 v, uint32_t 
       : "memory");
 }
 
+// Runs v through the folds of blocks r0 .. r1 - 1 of the round; where `in` is given, it is set
+// to what enters the lane's chunk of the last of them.  BACK: a tile's last chunk comes first.
+template <int SPLIT, bool BACK>
+__device__ __forceinline__ float2 carry_through(const FoldRow* row, int r0, int r1, float2 v,
+                                                float2* in) {
+  constexpr int kLanes = Shape<SPLIT>::kLanes;
+  const int lane = threadIdx.x & 31, part = lane / kLanes, cl = lane % kLanes;
+#pragma unroll 4
+  for (int r = r0; r < r1; ++r) {
+    float4 f[SPLIT];
+#pragma unroll
+    for (int i = 0; i < SPLIT; ++i) f[i] = row[r][kLanes * i + cl];
+#pragma unroll
+    for (int i = 0; i < SPLIT; ++i) {
+      const int h = BACK ? SPLIT - 1 - i : i;
+      if (in && h == part) *in = v;
+      v = fma2(first2(f[h]), v, last2(f[h]));
+    }
+  }
+  return v;
+}
 // One round of the carry, by one warp: own is the (A, H) of the lane's chunk of this block's
-// tile.  Returns what enters that chunk and moves `carry` behind the round's last chunk; BACK:
-// a tile's last chunk comes first.  `lost`: a wait has expired, later ones are not tried.
+// tile.  Returns what enters that chunk and moves `carry` behind this block's tile; carry_rest
+// moves it behind the round's other tiles, when nobody waits for it any more.  `lost`: a wait
+// has expired, later ones are not tried.
 template <int SPLIT, bool BACK>
 __device__ __forceinline__ float2 carry_round(const Chains& ch, int rank, int round, float4 own,
                                               CarrySmem& sm, FoldRow* folds, float2* carry,
                                               bool* lost) {
+  float2 in = *carry;
+  if (SPLIT == 1 && ch.cs == 1) {
+    *carry = fma2(first2(own), in, last2(own));
+    return in;
+  }
   const int lane = threadIdx.x & 31, buf = round & 1;
   FoldRow* row = folds + buf * ch.cs;
   if (ch.cs > 1) {
@@ -157,28 +184,20 @@ __device__ __forceinline__ float2 carry_round(const Chains& ch, int rank, int ro
       *lost = !__all_sync(0xffffffffu, ok);
       if (*lost && lane == 0) report_timeout(ch.status, 0x4c52);
     }
-  } else if (SPLIT > 1) {  // the parts' chunks
+  } else {  // the parts' chunks
     row[0][lane] = own;
     __syncwarp();
   }
-  float2 in = *carry, v = *carry;
-  if (SPLIT == 1 && ch.cs == 1) {
-    *carry = fma2(first2(own), in, last2(own));
-    return in;
-  }
-  constexpr int kLanes = Shape<SPLIT>::kLanes;
-  const int part = lane / kLanes, cl = lane % kLanes;
-  for (int r = 0; r < ch.cs; ++r) {
-#pragma unroll
-    for (int i = 0; i < SPLIT; ++i) {
-      const int h = BACK ? SPLIT - 1 - i : i;
-      if (r == rank && h == part) in = v;
-      const float4 f = row[r][kLanes * h + cl];
-      v = fma2(first2(f), v, last2(f));
-    }
-  }
-  *carry = v;
+  const float2 v = carry_through<SPLIT, BACK>(row, 0, rank, in, nullptr);
+  *carry = carry_through<SPLIT, BACK>(row, rank, rank + 1, v, &in);
   return in;
+}
+template <int SPLIT, bool BACK>
+__device__ __forceinline__ void carry_rest(const Chains& ch, int rank, int round,
+                                           const FoldRow* folds, float2* carry) {
+  if (ch.cs > 1)
+    *carry = carry_through<SPLIT, BACK>(folds + (round & 1) * ch.cs, rank + 1, ch.cs, *carry,
+                                        nullptr);
 }
 
 __device__ __forceinline__ void carry_begin(const Chains& ch, CarrySmem& sm) {
