@@ -530,10 +530,12 @@ static int validate_linrec(const LinrecArgs& p, int more_flags, long long* chunk
       if (p.cu[i + 1] < p.cu[i]) return GDN_ERR_INVALID_ARG;
   }
   *chunks = linrec_chunks(p.cu, p.B, p.T);
-  // chunk and tile numbers are 32-bit, and so are byte offsets inside a tile of 256 tokens
+  // token, chunk and block numbers are 32-bit, and so are byte offsets inside a tile of 256 tokens
+  const long long blocks = (p.D + 15) / 16;
+  if (p.T > 1 << 30 || *chunks * blocks > 0x3fffffffLL || p.B * blocks > 0x3fffffffLL)
+    return GDN_ERR_UNSUPPORTED;
   if (p.ldx > 1 << 21 || p.lda > 1 << 21 || p.ldb > 1 << 21 || p.D > 1 << 21)
     return GDN_ERR_UNSUPPORTED;
-  if (*chunks * ((p.D + 31) / 32) > 0x3fffffffLL) return GDN_ERR_UNSUPPORTED;
   if (p.B == 0 || *chunks == 0) return GDN_OK;
   const size_t es = elem_size(p.dtype), ges = (p.flags & GDN_GATES_PRECOMPUTED) ? 4 : es;
   if (!ok_elem(p.x, es) || !ok_elem(p.a, ges) || (p.b != nullptr && !ok_elem(p.b, ges)))

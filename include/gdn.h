@@ -500,8 +500,9 @@ size_t gdn2_chunk_workspace_bytes(int B, int T, int H, int dk, int dv, int dtype
  *   workspace / ws_bytes: device scratch owned by the caller, 16-byte aligned, at least
  *              gdn_linrec_workspace_bytes() bytes, overwritten -> else GDN_ERR_WORKSPACE.
  *              Calls that may run at the same time need a workspace each.
- *   Every pointer needs its element alignment only (rows that are 16-byte aligned move
- *   in 16-byte pieces).  States and sums are float32, outputs rounded once; the result
+ *   Every pointer needs its element alignment only (inputs whose rows are all 16-byte
+ *   aligned come by TMA).  At most 2^30 tokens, D and every ld at most 2^21, and fewer
+ *   than 2^30 pairs of a chunk and 16 channels: else GDN_ERR_UNSUPPORTED.  States and sums are float32, outputs rounded once; the result
  *   does not depend on how the work was split.  T = 0 and empty sequences copy h0 to ht
  *   (or zeros).  Long sequences of few channels are taken by clusters of thread blocks
  *   that wait for one another, with a limit: an expired wait is reported by
@@ -584,7 +585,8 @@ int gdn_linrec_step(const void* x, const void* a, const void* b, const float* A_
  *   d from 1 to 256, rot even, 0 <= rot <= d, 0 <= eps <= 1
  *   q_out, k_out: dtype, ldqo, ldko; written; may be q, k (same ld), must not otherwise
  *     overlap an input
- * float32 arithmetic, outputs rounded once.  Element alignment is enough.
+ * float32 arithmetic, outputs rounded once.  Element alignment is enough (rows of whole
+ * 16-byte pieces move in them).  At most 2^30 tokens and 2^20 heads.
  */
 int gdn_qk_norm_rope(const void* q, const void* k, const long long* positions,
                      const float* inv_freq, const float* q_weight, const float* k_weight,

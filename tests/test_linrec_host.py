@@ -39,9 +39,17 @@ def test_forward_rejects(kw):
 
 def test_forward_limits():
     assert fwd(T=2 ** 31 - 1, D=2 ** 20, ldx=2 ** 20, lda=2 ** 20, ldb=2 ** 20, ldh=2 ** 20) == -2
+    for kw in (dict(T=2 ** 30 + 1), dict(D=2 ** 21 + 1, ldx=2 ** 22, lda=2 ** 22, ldb=2 ** 22),
+               dict(ldx=2 ** 21 + 1), dict(lda=2 ** 30), dict(ldb=2 ** 40), dict(ldh=2 ** 22),
+               dict(B=2 ** 30, T=1)):
+        assert fwd(**kw) == -2, kw
     need = G.gdn_linrec_workspace_bytes(2, 100, 64)
-    for ws, n in ((FAKE, need - 1), (None, need), (FAKE + 8, need)) if need else ():
-        assert fwd(ws=ws, n=n) == -5
+    assert need == 0  # only packed batches take one
+    cu = offsets(0, 40, 100)
+    need = L.gdn_linrec_workspace_bytes(cu, 2, 100, 64)
+    assert need > 0
+    for ws, n in ((FAKE, need - 1), (None, need), (FAKE + 8, need)):
+        assert fwd(cu=cu, ws=ws, n=n) == -5
     assert fwd(B=0, cu=None) == 0                      # no sequence, nothing to write
     assert fwd(B=2, T=0, x=None, a=None, h=None) == 0  # no token, no final state wanted
 
