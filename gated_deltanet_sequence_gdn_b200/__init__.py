@@ -811,7 +811,9 @@ def gdn_linrec_fwd(x, a, b=None, A_log=None, dt_bias=None, h0=None, *, cu_seqlen
     odt = f32 if out_f32 else x.dtype
     if h is None:
         h = _new(x, odt)
-    ph, ldh = _strided(h, odt, x.shape, dev, "h")
+        ph, ldh = h.data_ptr(), D
+    else:
+        ph, ldh = _strided(h, odt, x.shape, dev, "h")
     if ht is None and want_ht:
         ht = x.new_empty((B, D), dtype=f32) if h0 is None else torch.empty_like(h0)
     if want_states or states is not None:
@@ -879,12 +881,15 @@ def gdn_linrec_step(x, a, b, A_log, dt_bias, state, *, input_scale="none",
     N, D = x.shape
     ins, lds, flags = _linrec_inputs(x, a, b, A_log, dt_bias, gates_precomputed, input_scale)
     odt = torch.float32 if out_f32 else x.dtype
+    dev = x.device
     if h is None:
         h = _new(x, odt)
-    ph, ldh = _strided(h, odt, (N, D), x.device, "h")
-    _check(lib.gdn_linrec_step(*ins, _dense(state, torch.float32, (N, D), x.device, "state"), N,
-                               D, *lds, _dtype_code(x.dtype), flags | (OUT_F32 if out_f32 else 0),
-                               ph, ldh, _here(x.device)), "gdn_linrec_step")
+        ph, ldh = h.data_ptr(), D
+    else:
+        ph, ldh = _strided(h, odt, x.shape, dev, "h")
+    _check(lib.gdn_linrec_step(*ins, _dense(state, torch.float32, x.shape, dev, "state"), N, D,
+                               *lds, _dtype_code(x.dtype), flags | (OUT_F32 if out_f32 else 0),
+                               ph, ldh, _here(dev)), "gdn_linrec_step")
     return h
 
 
@@ -915,6 +920,18 @@ def _rope_inputs(q, k, positions, inv_freq, q_weight, k_weight, norm, interleave
     return (pq, pk, pp, pf, *pw, tokens, Hq, Hk, d, rot, ldq, ldk), flags, dt, dev, lead
 
 
+def _rope_out(t, out, dt, dev, name):
+    """(output like t, pointer, elements from token to token)."""
+    if t is None:
+        if out is not None:
+            raise ValueError(f"{name}: given without its input")
+        return None, None, 0
+    if out is None:
+        out = _new(t, dt)
+        return out, out.data_ptr(), t.shape[-1] * t.shape[-2]
+    return out, *_strided(out, dt, t.shape, dev, name, 2)
+
+
 def gdn_qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, *, norm="rms",
                      eps=1e-6, scale=1.0, interleaved=False, q_out=None, k_out=None,
                      stream=None):
@@ -932,12 +949,8 @@ def _rope_fwd(_, q, k, positions, inv_freq, q_weight, k_weight, norm, eps, scale
               q_out, k_out):
     args, flags, dt, dev, lead = _rope_inputs(q, k, positions, inv_freq, q_weight, k_weight,
                                               norm, interleaved)
-    if q is not None and q_out is None:
-        q_out = _new(q, dt)
-    if k is not None and k_out is None:
-        k_out = _new(k, dt)
-    po = _strided(q_out, dt, () if q is None else q.shape, dev, "q_out", 2)
-    ko = _strided(k_out, dt, () if k is None else k.shape, dev, "k_out", 2)
+    q_out, *po = _rope_out(q, q_out, dt, dev, "q_out")
+    k_out, *ko = _rope_out(k, k_out, dt, dev, "k_out")
     _check(lib.gdn_qk_norm_rope(*args, _dtype_code(dt), flags, eps, scale, *po, *ko,
                                 _here(dev)), "gdn_qk_norm_rope")
     return q_out, k_out
