@@ -83,6 +83,7 @@ linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
   bool lost = false;
   Rows<TO> out;
   out.begin(p.h, p.ldh, k.tok + k.rank * kTileT, k.c0, at.first, 2 * at.cl);
+  const bool alone = SPLIT == 1 && ch.cs == 1;  // what enters a tile is known before it is folded
   const int rounds = (k.tiles + ch.cs - 1) / ch.cs;
   for (int round = 0; round < rounds; ++round) {
     const int n = length(round);
@@ -139,25 +140,26 @@ linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
     carry_sm.fold[threadIdx.x] = join4(A, H);
     __syncthreads();
     if (at.warp == 0) {
-      A = both(1.f);
-      H = both(0.f);
-#pragma unroll 4
-      for (int w = 0; w < 8; ++w) {
-        const float4 f = carry_sm.fold[at.group(w)];
-        H = fma2(first2(f), H, last2(f));
-        A = mul2(A, first2(f));
-      }
-      float2 v = carry_round<SPLIT, false>(ch, k.rank, round, join4(A, H), carry_sm, folds, &carry,
-                                            &lost);
+      float2 v = carry;
+      if (!alone)
+        v = carry_round<SPLIT, false>(ch, k.rank, round,
+                                      chunk_fold<SPLIT, false>(at, carry_sm, nullptr), carry_sm,
+                                      folds, &carry, &lost);
       if (n > at.part * kLinrecChunk)
         write2(p.states_out,
                k.chunk0 + (long long)(round * ch.cs + k.rank) * kTileChunks + at.part, c, p.D, v);
+      A = both(1.f);
+      H = both(0.f);
 #pragma unroll 4
       for (int w = 0; w < 8; ++w) {
         carry_sm.start[at.group(w)] = v;
         const float4 f = carry_sm.fold[at.group(w)];
         v = fma2(first2(f), v, last2(f));
+        H = fma2(first2(f), H, last2(f));
+        A = mul2(A, first2(f));
       }
+      // what leaves the tile, as it is formed elsewhere: from the chunk's own (A, H)
+      if (alone) carry = fma2(A, carry, H);
     }
     __syncthreads();
     if (p.h) {

@@ -98,6 +98,7 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
   odx.begin(p.dx, p.lddx, tok0, k.c0, first, 2 * at.cl);
   oda.begin(p.da, p.ldda, tok0, k.c0, first, 2 * at.cl);
   odb.begin(p.db, p.lddb, tok0, k.c0, first, 2 * at.cl);
+  const bool alone = SPLIT == 1 && ch.cs == 1;  // what enters a tile is known before it is folded
   const int rounds = (k.tiles + ch.cs - 1) / ch.cs;
   for (int round = 0; round < rounds; ++round) {
     const int tt = tile(round), n = length(round);
@@ -174,21 +175,21 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
         hs = fma2(first2(q), hs, last2(q));
       }
     } else if (at.warp == 0) {  // its gradient
-      float2 A = both(1.f), R = both(0.f);
+      float2 v = carry, A = both(1.f), R = both(0.f);
+      if (!alone)
+        v = carry_round<SPLIT, true>(ch, k.rank, round,
+                                     chunk_fold<SPLIT, true>(at, sm.carry, sm.back), sm.carry,
+                                     folds, &carry, &lost);
 #pragma unroll 4
       for (int w = 7; w >= 0; --w) {
-        const float2 a = first2(sm.carry.fold[at.group(w)]);
-        R = fma2(a, R, sm.back[at.group(w)]);
+        const float2 r = sm.back[at.group(w)], a = first2(sm.carry.fold[at.group(w)]);
+        sm.back[at.group(w)] = v;
+        v = fma2(a, v, r);
+        R = fma2(a, R, r);
         A = mul2(A, a);
       }
-      float2 v = carry_round<SPLIT, true>(ch, k.rank, round, join4(A, R), sm.carry, folds, &carry,
-                                           &lost);
-#pragma unroll 4
-      for (int w = 7; w >= 0; --w) {
-        const float2 r = sm.back[at.group(w)];
-        sm.back[at.group(w)] = v;
-        v = fma2(first2(sm.carry.fold[at.group(w)]), v, r);
-      }
+      // what leaves the tile, as it is formed elsewhere: from the chunk's own (A, R)
+      if (alone) carry = fma2(A, carry, R);
     }
     __syncthreads();
     hs = sm.carry.start[threadIdx.x];

@@ -109,9 +109,14 @@ struct Split {
 inline long long chains_of(const LinrecArgs& p, int split) {
   return (long long)p.B * ((p.D * (long long)split + 63) / 64);
 }
-// The one of the three shapes that has the most blocks at work at once: whole chunks of 64
-// channels where those chains fill the machine; else the largest cluster whose launch still
-// runs at once, the smaller cluster (fewer exchanges) where shapes are equal.
+// Whole chunks of 64 channels where those chains fill the machine (608 to 704 chains of 4096
+// tokens take the same 286 us without clusters; in clusters, which end in a smaller last wave,
+// 286 to 341).  Elsewhere the one of the three shapes that has the most blocks at work at once:
+// the largest cluster whose launch still runs at once, the smaller cluster (fewer exchanges)
+// where shapes are equal.  Forward, us by shape (chunks of a tile x blocks of a cluster):
+//   8192 tokens x 12288 channels  1x1 273, 1x2 200, 2x1 191 (taken), 1x4 206 (two waves)
+//   131072 x 1024                 1x16 444, 2x8 356, 4x8 296 (taken), 4x16 610 (two waves)
+//   8192 x 4096                   1x1 212, 1x4 87, 1x6 80, 2x3 80, 4x1 84
 template <typename K>
 cudaError_t choose_split(const LinrecArgs& p, K k1, K k2, K k4, size_t smem, size_t most_smem,
                          KernelSlots* known, Split* out) {

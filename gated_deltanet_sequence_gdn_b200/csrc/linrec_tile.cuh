@@ -136,6 +136,20 @@ __device__ __forceinline__ void st_async_peer(uint32_t addr, float4 v, uint32_t 
       : "memory");
 }
 
+// (A, H) of the lane's chunk, from the folds of its 8 groups of tokens; BACK: (A, R).
+template <int SPLIT, bool BACK>
+__device__ __forceinline__ float4 chunk_fold(const Spot<SPLIT>& at, const CarrySmem& sm,
+                                             const float2* back) {
+  float2 A = both(1.f), H = both(0.f);
+#pragma unroll 4
+  for (int i = 0; i < 8; ++i) {
+    const int j = at.group(BACK ? 7 - i : i);
+    const float4 f = sm.fold[j];
+    H = fma2(first2(f), H, BACK ? back[j] : last2(f));
+    A = mul2(A, first2(f));
+  }
+  return join4(A, H);
+}
 // Runs v through the folds of blocks r0 .. r1 - 1 of the round; where `in` is given, it is set
 // to what enters the lane's chunk of the last of them.  BACK: a tile's last chunk comes first.
 template <int SPLIT, bool BACK>
