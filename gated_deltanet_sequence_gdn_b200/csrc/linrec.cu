@@ -54,11 +54,12 @@ linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
     const int left = tokens - round * step;
     return left < kTileT ? (left < 0 ? 0 : left) : kTileT;
   };
+  bool late = false;  // a tile has not come in time: no more are asked for
   auto load = [&](int round) {
     const int n = length(round), t = (round * ch.cs + k.rank) * kTileT;
     const FwdStage<TX, TG> st = stage(round);
     if (ch.tma) {
-      if (n > 0 && threadIdx.x == 0) {
+      if (n > 0 && threadIdx.x == 0 && !late) {
         uint64_t* bar = &carry_sm.loaded[round & 1];
         const int y = ch.tab.cu ? (int)k.tok + t : t, z = ch.tab.cu ? 0 : k.row;
         tc::mbar_arrive_expect_tx(bar, stage_size);
@@ -89,8 +90,10 @@ linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
     const int n = length(round);
     if (!ch.tma) {
       cp_async_wait<0>();
-    } else if (n > 0 && !tc::mbar_wait(&carry_sm.loaded[round & 1], (round >> 1) & 1, nullptr, 0)) {
+    } else if (n > 0 && !late &&
+               !tc::mbar_wait(&carry_sm.loaded[round & 1], (round >> 1) & 1, nullptr, 0)) {
       report_timeout(ch.status, 0x4c54);
+      late = true;
     }
     __syncthreads();  // the stage is complete, the other one free
     if (round + 1 < rounds) load(round + 1);

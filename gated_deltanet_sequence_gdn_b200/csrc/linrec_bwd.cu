@@ -56,11 +56,12 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
   auto length = [&](int round) {  // of the round's tile: only the sequence's last is short
     return tile(round) < 0 ? 0 : round == 0 && tokens < kTileT ? tokens : kTileT;
   };
+  bool late = false;  // a tile has not come in time: no more are asked for
   auto load = [&](int round) {
     const int n = length(round), t = tile(round) * kTileT;
     BwdStage<TX, TG, TD>& st = sm.stage[round % kStages];
     if (ch.tma) {
-      if (n > 0 && threadIdx.x == 0) {
+      if (n > 0 && threadIdx.x == 0 && !late) {
         uint64_t* bar = &sm.carry.loaded[round % kStages];
         const int y = ch.tab.cu ? (int)k.tok + t : t, z = ch.tab.cu ? 0 : k.row;
         tc::mbar_arrive_expect_tx(bar, sizeof(st.x) + sizeof(st.a) + (p.b ? sizeof(st.b) : 0) +
@@ -104,9 +105,11 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
     const int tt = tile(round), n = length(round);
     if (!ch.tma) {
       cp_async_wait<0>();
-    } else if (n > 0 && !tc::mbar_wait(&sm.carry.loaded[round % kStages], (round / kStages) & 1,
-                                       nullptr, 0)) {
+    } else if (n > 0 && !late &&
+               !tc::mbar_wait(&sm.carry.loaded[round % kStages], (round / kStages) & 1, nullptr,
+                              0)) {
       report_timeout(ch.status, 0x4c54);
+      late = true;
     }
     __syncthreads();  // the stage is complete, the other one free
     if (kStages > 1 && round + 1 < rounds) load(round + 1);

@@ -187,13 +187,15 @@ __device__ __forceinline__ float2 carry_round(const Chains& ch, int rank, int ro
   const int lane = threadIdx.x & 31, buf = round & 1;
   FoldRow* row = folds + buf * ch.cs;
   if (ch.cs > 1) {
-    if (lane == 0)
-      tc::mbar_arrive_expect_tx(&sm.full[buf], (uint32_t)(ch.cs * 32 * sizeof(float4)));
-    __syncwarp();
-    if (!*lost && !(ch.fault && rank == 0))  // nothing is under way to a peer that has given up
-      for (int r = 0; r < ch.cs; ++r)
-        st_async_peer(tc::map_peer(&row[rank][lane], r), own, tc::map_peer(&sm.full[buf], r));
+    // Once a wait has expired its phase stays open: nothing is armed on it again (an arrival in
+    // a phase that expects none is undefined), nothing sent, nothing waited for.
     if (!*lost) {
+      if (lane == 0)
+        tc::mbar_arrive_expect_tx(&sm.full[buf], (uint32_t)(ch.cs * 32 * sizeof(float4)));
+      __syncwarp();
+      if (!(ch.fault && rank == 0))
+        for (int r = 0; r < ch.cs; ++r)
+          st_async_peer(tc::map_peer(&row[rank][lane], r), own, tc::map_peer(&sm.full[buf], r));
       const bool ok = tc::mbar_wait(&sm.full[buf], (round >> 1) & 1, nullptr, 0, ch.spin);
       *lost = !__all_sync(0xffffffffu, ok);
       if (*lost && lane == 0) report_timeout(ch.status, 0x4c52);

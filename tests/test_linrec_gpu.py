@@ -402,10 +402,11 @@ def test_refused_tensors():
         G.gdn_linrec_bwd(*ok, d["dh"], d["dht"], states=torch.zeros(1, 16, device="cuda"))
 
 
-def test_an_expired_wait_is_reported():
-    """The first chunks keep their states to themselves: the waits behind them end and say so,
-    and the next call is right again."""
-    _, d = make(2, 300, 70, F32, seed=16)
+@pytest.mark.parametrize("T", [300, 5000])
+def test_an_expired_wait_is_reported(T):
+    """The first block of each cluster keeps its chunks' results to itself: the waits of the
+    others end and say so, in one round or over several, and the next call is right again."""
+    _, d = make(2, T, 70, F32, seed=16)
     h, ht, st = G.gdn_linrec_fwd(*ins(d), want_states=True)
     g = G.gdn_linrec_bwd(*ins(d), d["dh"], d["dht"], states=st)
     torch.cuda.synchronize()
