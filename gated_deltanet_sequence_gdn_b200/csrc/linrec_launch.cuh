@@ -109,32 +109,37 @@ struct Split {
 inline long long chains_of(const LinrecArgs& p, int split) {
   return (long long)p.B * ((p.D * (long long)split + 63) / 64);
 }
-// Whole chunks of 64 channels where those chains fill the machine (608 to 704 chains of 4096
-// tokens take the same 286 us without clusters; in clusters, which end in a smaller last wave,
-// 286 to 341).  Elsewhere the one of the three shapes that has the most blocks at work at once:
-// the largest cluster whose launch still runs at once, the smaller cluster (fewer exchanges)
-// where shapes are equal.  Forward, us by shape (chunks of a tile x blocks of a cluster):
-//   8192 tokens x 12288 channels  1x1 273, 1x2 200, 2x1 191 (taken), 1x4 206 (two waves)
+// The shape that keeps the most of the machine at useful work: blocks at work at once times
+// the share of a tile's channels that exist.  Chains that fill the machine run without
+// clusters (608 to 704 chains of 4096 tokens take the same 286 us; in clusters, which end in a
+// smaller last wave, 286 to 341); fewer run in the largest cluster whose launch still runs at
+// once, and the smaller cluster (fewer exchanges) is taken where shapes are equal.  Forward, us
+// by shape (chunks of a tile x blocks of a cluster):
+//   8192 tokens x 12288 channels  1x1 273, 1x2 200, 2x1 191, 4x1 191 (768 blocks), 1x4 206
 //   131072 x 1024                 1x16 444, 2x8 356, 4x8 296 (taken), 4x16 610 (two waves)
-//   8192 x 4096                   1x1 212, 1x4 87, 1x6 80, 2x3 80, 4x1 84
+//   8192 x 4096                   1x1 212, 1x4 87, 1x6 80, 2x3 80 (taken), 4x1 84
 template <typename K>
 cudaError_t choose_split(const LinrecArgs& p, K k1, K k2, K k4, size_t smem, size_t most_smem,
                          KernelSlots* known, Split* out) {
   *out = Split{1, 1};
   const long long chunks = (longest(p) + kLinrecChunk - 1) / kLinrecChunk;
-  long long best = 0;
+  const long long mean = p.cu ? linrec_chunks(p.cu, p.B, p.T) / p.B : chunks;
+  double best = 0.0;
   for (int j = 0; j < 3; ++j) {
     const int split = 1 << j;
+    if (j > 0 && mean < split) break;  // tiles of more chunks than a sequence has
     const std::atomic<int>* slots = nullptr;
     cudaError_t e = kernel_slots(j == 0 ? k1 : j == 1 ? k2 : k4, smem, most_smem, known + j, &slots);
     if (e != cudaSuccess) return e;
     const long long n = chains_of(p, split), tiles = (chunks + split - 1) / split;
-    if (n > slots[1].load(std::memory_order_relaxed) || (j > 0 && chunks < split)) break;
+    const long long room = slots[1].load(std::memory_order_relaxed);
     int cs = 1;
     for (int i = 2; i <= kMaxCluster && i <= tiles; ++i)
       if (n <= slots[i].load(std::memory_order_relaxed)) cs = i;
-    if (n * cs > best || (n * cs == best && cs < out->cs)) {
-      best = n * cs;
+    const double used = (double)p.B * p.D * split / (64.0 * n);
+    const double work = used * (double)(n > room ? room : n * cs);
+    if (work > 1.02 * best || (work > 0.98 * best && cs < out->cs)) {
+      best = work > best ? work : best;
       *out = Split{split, cs};
     }
   }
