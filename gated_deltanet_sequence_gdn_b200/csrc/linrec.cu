@@ -32,7 +32,7 @@ struct FwdStage {
   TG *a, *b;
 };
 
-template <typename TX, typename TG, bool GIVEN, int SCALE, typename TO, int SPLIT>
+template <typename TX, typename TG, bool GIVEN, int SCALE, typename TO, int SPLIT, bool CLUSTER>
 __global__ void __launch_bounds__(kLinrecThreads, sizeof(TX) + sizeof(TG) == 4 ? 4 : 2)
 linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ LinrecMaps maps) {
   extern __shared__ __align__(128) unsigned char smem_raw[];
@@ -46,9 +46,9 @@ linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
   };
   constexpr int kTileT = Shape<SPLIT>::kT, kC = Shape<SPLIT>::kC, kTileChunks = kTileT / kLinrecChunk;
   const Spot<SPLIT> at;
-  const Chain k = chain_of<SPLIT>(p, ch);
+  const Chain k = chain_of<SPLIT, CLUSTER>(p, ch);
   const int c = k.c0 + 2 * at.cl, cols = p.D - c;
-  const int step = ch.cs * kTileT;
+  const int cs = CLUSTER ? ch.cs : 1, step = cs * kTileT;
   const int tokens = (int)k.len - k.rank * kTileT;  // from the block's first tile on
   auto length = [&](int round) {
     const int left = tokens - round * step;
@@ -56,7 +56,7 @@ linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
   };
   bool late = false;  // a tile has not come in time: no more are asked for
   auto load = [&](int round) {
-    const int n = length(round), t = (round * ch.cs + k.rank) * kTileT;
+    const int n = length(round), t = (round * cs + k.rank) * kTileT;
     const FwdStage<TX, TG> st = stage(round);
     if (ch.tma) {
       if (n > 0 && threadIdx.x == 0 && !late) {
@@ -76,7 +76,7 @@ linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
       cp_async_commit();
     }
   };
-  carry_begin(ch, carry_sm);
+  carry_begin<CLUSTER>(carry_sm);
   load(0);
   GateConst gc{both(0.f), both(0.f)};
   if (!GIVEN) gc = gate_const(p.A_log, p.dt_bias, c, p.D);
@@ -84,8 +84,8 @@ linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
   bool lost = false;
   Rows<TO> out;
   out.begin(p.h, p.ldh, k.tok + k.rank * kTileT, k.c0, at.first, 2 * at.cl);
-  const bool alone = SPLIT == 1 && ch.cs == 1;  // what enters a tile is known before it is folded
-  const int rounds = (k.tiles + ch.cs - 1) / ch.cs;
+  constexpr bool alone = SPLIT == 1 && !CLUSTER;  // what enters a tile is known before it is folded
+  const int rounds = (k.tiles + cs - 1) / cs;
   for (int round = 0; round < rounds; ++round) {
     const int n = length(round);
     if (!ch.tma) {
@@ -104,13 +104,13 @@ linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
     for (int i0 = 0; i0 < kPer; i0 += kGroup) {
       float2 e[kGroup];
 #pragma unroll
-      for (int i = 0; i < kGroup; ++i) e[i] = get2(st.a + mine + (i0 + i) * kC);
-      decay_exponents<GIVEN, kGroup>(e, gc);
-#pragma unroll
       for (int i = 0; i < kGroup; ++i) {
-        al[i0 + i] = ex2_2(e[i]);
+        e[i] = get2(st.a + mine + (i0 + i) * kC);
         u[i0 + i] = get2(st.x + mine + (i0 + i) * kC);
       }
+      decay_exponents<GIVEN, kGroup>(e, gc);
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i) al[i0 + i] = ex2_2(e[i]);
       if (SCALE != kScaleNone) {
         float2 f[kGroup];
         input_scales<SCALE, kGroup>(e, al + i0, f);
@@ -145,12 +145,12 @@ linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
     if (at.warp == 0) {
       float2 v = carry;
       if (!alone)
-        v = carry_round<SPLIT, false>(ch, k.rank, round,
-                                      chunk_fold<SPLIT, false>(at, carry_sm, nullptr), carry_sm,
-                                      folds, &carry, &lost);
+        v = carry_round<SPLIT, CLUSTER, false>(
+            ch, k.rank, round, chunk_fold<SPLIT, false>(at, carry_sm, nullptr), carry_sm, folds,
+            &carry, &lost);
       if (n > at.part * kLinrecChunk)
         write2(p.states_out,
-               k.chunk0 + (long long)(round * ch.cs + k.rank) * kTileChunks + at.part, c, p.D, v);
+               k.chunk0 + (long long)(round * cs + k.rank) * kTileChunks + at.part, c, p.D, v);
       A = both(1.f);
       H = both(0.f);
 #pragma unroll 4
@@ -182,10 +182,10 @@ linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
       }
       out.advance(step);
     }
-    if (at.warp == 0) carry_rest<SPLIT, false>(ch, k.rank, round, folds, &carry);
+    if (at.warp == 0) carry_rest<SPLIT, CLUSTER, false>(ch, k.rank, round, folds, &carry);
   }
   if (k.rank == 0 && at.warp == 0 && at.part == 0) write2(p.ht, k.row, c, p.D, carry);
-  carry_end(ch);
+  carry_end<CLUSTER>();
 }
 
 // The step: HBM-bound on the float32 state, read and written once.  A thread takes 4 channels
@@ -323,16 +323,20 @@ struct FwdRun {
     using TO = typename Wide<TX, WIDE>::type;
     static KernelSlots known[2][3];  // with and without a write gate
     KernelSlots* k = known[p.b != nullptr];
-    const auto k1 = linrec_fwd_kernel<TX, TG, GIVEN, SCALE, TO, 1>;
-    const auto k2 = linrec_fwd_kernel<TX, TG, GIVEN, SCALE, TO, 2>;
-    const auto k4 = linrec_fwd_kernel<TX, TG, GIVEN, SCALE, TO, 4>;
+    using Kernel = void (*)(LinrecArgs, Chains, int, LinrecMaps);
+    const ChainKernel<Kernel> ks[3] = {{linrec_fwd_kernel<TX, TG, GIVEN, SCALE, TO, 1, false>,
+                                        linrec_fwd_kernel<TX, TG, GIVEN, SCALE, TO, 1, true>},
+                                       {linrec_fwd_kernel<TX, TG, GIVEN, SCALE, TO, 2, false>,
+                                        linrec_fwd_kernel<TX, TG, GIVEN, SCALE, TO, 2, true>},
+                                       {linrec_fwd_kernel<TX, TG, GIVEN, SCALE, TO, 4, false>,
+                                        linrec_fwd_kernel<TX, TG, GIVEN, SCALE, TO, 4, true>}};
     Split sp;
-    cudaError_t e = choose_split(p, k1, k2, k4, fwd_smem<TX, TG>(p.b != nullptr),
-                                 fwd_smem<TX, TG>(true), k, &sp);
+    cudaError_t e = choose_split(p, ks, fwd_smem<TX, TG>(p.b != nullptr), fwd_smem<TX, TG>(true), k,
+                                 &sp);
     if (e != cudaSuccess) return e;
-    return sp.split == 4   ? launch<TX, TG, 4>(k4, sp.cs)
-           : sp.split == 2 ? launch<TX, TG, 2>(k2, sp.cs)
-                           : launch<TX, TG, 1>(k1, sp.cs);
+    return sp.split == 4   ? launch<TX, TG, 4>(ks[2].of(sp.cs), sp.cs)
+           : sp.split == 2 ? launch<TX, TG, 2>(ks[1].of(sp.cs), sp.cs)
+                           : launch<TX, TG, 1>(ks[0].of(sp.cs), sp.cs);
   }
   template <typename TX, typename TG, int SPLIT, typename K>
   cudaError_t launch(K kernel, int cs) const {

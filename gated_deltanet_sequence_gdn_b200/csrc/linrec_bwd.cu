@@ -34,7 +34,7 @@ __device__ __forceinline__ void add_kept(float2* sum, float2* err, float2 v) {
   *sum = t;
 }
 
-template <typename TX, typename TG, bool GIVEN, int SCALE, typename TD, typename TDG, int SPLIT>
+template <typename TX, typename TG, bool GIVEN, int SCALE, typename TD, typename TDG, int SPLIT, bool CLUSTER>
 __global__ void __launch_bounds__(kLinrecThreads, 2)
 linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ LinrecMaps maps,
                   const float* states, float2* sums) {
@@ -46,13 +46,13 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
   constexpr int kTileT = Shape<SPLIT>::kT, kC = Shape<SPLIT>::kC, kTileChunks = kTileT / kLinrecChunk;
   const Spot<SPLIT> at;
   const int first = at.first;
-  const Chain k = chain_of<SPLIT>(p, ch);
+  const Chain k = chain_of<SPLIT, CLUSTER>(p, ch);
   const int c = k.c0 + 2 * at.cl, cols = p.D - c;
-  const int step = ch.cs * kTileT;
+  const int cs = CLUSTER ? ch.cs : 1, step = cs * kTileT;
   const int last = k.tiles - 1 - k.rank;  // the block's first tile; may be before the sequence
   const long long tok0 = k.tok + last * (long long)kTileT;
   const int tokens = (int)k.len - last * kTileT;  // from there to the sequence's end
-  auto tile = [&](int round) { return last - round * ch.cs; };
+  auto tile = [&](int round) { return last - round * cs; };
   auto length = [&](int round) {  // of the round's tile: only the sequence's last is short
     return tile(round) < 0 ? 0 : round == 0 && tokens < kTileT ? tokens : kTileT;
   };
@@ -81,7 +81,7 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
       cp_async_commit();
     }
   };
-  carry_begin(ch, sm.carry);
+  carry_begin<CLUSTER>(sm.carry);
   load(0);
   GateConst gc{both(0.f), both(0.f)};
   if (!GIVEN) gc = gate_const(p.A_log, p.dt_bias, c, p.D);
@@ -99,8 +99,8 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
   odx.begin(p.dx, p.lddx, tok0, k.c0, first, 2 * at.cl);
   oda.begin(p.da, p.ldda, tok0, k.c0, first, 2 * at.cl);
   odb.begin(p.db, p.lddb, tok0, k.c0, first, 2 * at.cl);
-  const bool alone = SPLIT == 1 && ch.cs == 1;  // what enters a tile is known before it is folded
-  const int rounds = (k.tiles + ch.cs - 1) / ch.cs;
+  constexpr bool alone = SPLIT == 1 && !CLUSTER;  // what enters a tile is known before it is folded
+  const int rounds = (k.tiles + cs - 1) / cs;
   for (int round = 0; round < rounds; ++round) {
     const int tt = tile(round), n = length(round);
     if (!ch.tma) {
@@ -114,7 +114,7 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
     __syncthreads();  // the stage is complete, the other one free
     if (kStages > 1 && round + 1 < rounds) load(round + 1);
     float2 hs = hnext;  // warp 1's
-    if (at.warp == 1) hnext = state(tt - ch.cs);
+    if (at.warp == 1) hnext = state(tt - cs);
     BwdStage<TX, TG, TD>& st = sm.stage[round % kStages];
     if (n > 0 && n < kTileT && ch.tab.cu) {  // the next sequence's tokens
       clear_rows<SPLIT>(st.x, n);
@@ -123,6 +123,7 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
     }
     const int mine = at.mine();
     float2 e[kPer], slope[kPer], be[kPer];
+    float2 Am, Hm;  // of the first kGroup tokens
     {
       float2 al[kPer], A = both(1.f), H = both(0.f), R = both(0.f);
 #pragma unroll
@@ -154,6 +155,10 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
           H = fma2(al[i0 + i], H, u);
           A = mul2(A, al[i0 + i]);
         }
+        if (i0 == 0) {
+          Am = A;
+          Hm = H;
+        }
       }
       if (n == kTileT) {
 #pragma unroll
@@ -180,9 +185,9 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
     } else if (at.warp == 0) {  // its gradient
       float2 v = carry, A = both(1.f), R = both(0.f);
       if (!alone)
-        v = carry_round<SPLIT, true>(ch, k.rank, round,
-                                     chunk_fold<SPLIT, true>(at, sm.carry, sm.back), sm.carry,
-                                     folds, &carry, &lost);
+        v = carry_round<SPLIT, CLUSTER, true>(
+            ch, k.rank, round, chunk_fold<SPLIT, true>(at, sm.carry, sm.back), sm.carry, folds,
+            &carry, &lost);
 #pragma unroll 4
       for (int w = 7; w >= 0; --w) {
         const float2 r = sm.back[at.group(w)], a = first2(sm.carry.fold[at.group(w)]);
@@ -196,68 +201,67 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
     }
     __syncthreads();
     hs = sm.carry.start[threadIdx.x];
-    float2 al[kPer], f[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) al[i] = ex2_2(e[i]);
-    if (SCALE != kScaleNone) {
-#pragma unroll
-      for (int i0 = 0; i0 < kPer; i0 += kGroup)
-        input_scales<SCALE, kGroup>(e + i0, al + i0, f + i0);
-    }
-    float2 hp[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      hp[i] = hs;
-      float2 u = mul2(get2(st.x + mine + i * kC), be[i]);
-      if (SCALE != kScaleNone) u = mul2(u, f[i]);
-      hs = fma2(al[i], hs, u);
-    }
     float2 cc = sm.back[threadIdx.x];
     float2 tA = both(0.f), tb = both(0.f);
-    auto token = [&](int i, float2* dx, float2* da, float2* db) {
-      const int el = mine + i * kC;
-      const float2 lam = add2(get2(st.dh + el), cc);
-      cc = mul2(al[i], lam);
-      const float2 lx = mul2(lam, get2(st.x + el));
-      float2 dg = mul2(cc, hp[i]);
-      *dx = mul2(lam, be[i]);
-      *db = lx;
-      if (SCALE != kScaleNone) {
-        const float2 q = make_float2(input_scale_slope<SCALE>(al[i].x, f[i].x),
-                                     input_scale_slope<SCALE>(al[i].y, f[i].y));
-        dg = fma2(mul2(lx, be[i]), q, dg);
-        *dx = mul2(*dx, f[i]);
-        *db = mul2(*db, f[i]);
-      }
-      *da = dg;
-      if (!GIVEN) {
-        if (p.b) *db = mul2(mul2(*db, be[i]), write_gate_rest(get2(st.b + el), be[i]));
-        *da = mul2(dg, slope[i]);
-        tb = add2(tb, *da);
-        // dg log2(e) times e, which is -inf where alpha = 0
-        tA = fma2(dg, make_float2(fmaxf(e[i].x, -3e38f), fmaxf(e[i].y, -3e38f)), tA);
-      }
-    };
-    float2 dx, da, db;
-    if (n == kTileT && cols > 1 && vec) {
+    // The later group of tokens first; its states from the one in front of it.
 #pragma unroll
-      for (int i = kPer - 1; i >= 0; --i) {
-        token(i, &dx, &da, &db);
-        put2(odx.at(i), dx);
-        put2(oda.at(i), da);
-        if (p.b) put2(odb.at(i), db);
-      }
-    } else {
+    for (int i0 = kPer - kGroup; i0 >= 0; i0 -= kGroup) {
+      float2 al[kGroup], f[kGroup], hp[kGroup];
 #pragma unroll
-      for (int i = kPer - 1; i >= 0; --i) {
-        if (first + i >= n) continue;
-        token(i, &dx, &da, &db);
-        put2(odx.at(i), dx, cols);
-        put2(oda.at(i), da, cols);
-        if (p.b) put2(odb.at(i), db, cols);
+      for (int i = 0; i < kGroup; ++i) al[i] = ex2_2(e[i0 + i]);
+      if (SCALE != kScaleNone) input_scales<SCALE, kGroup>(e + i0, al, f);
+      hp[0] = i0 == 0 ? hs : fma2(Am, hs, Hm);
+#pragma unroll
+      for (int i = 0; i + 1 < kGroup; ++i) {
+        float2 u = mul2(get2(st.x + mine + (i0 + i) * kC), be[i0 + i]);
+        if (SCALE != kScaleNone) u = mul2(u, f[i]);
+        hp[i + 1] = fma2(al[i], hp[i], u);
+      }
+      auto token = [&](int j, float2* dx, float2* da, float2* db) {
+        const int i = i0 + j, el = mine + i * kC;
+        const float2 lam = add2(get2(st.dh + el), cc);
+        cc = mul2(al[j], lam);
+        const float2 lx = mul2(lam, get2(st.x + el));
+        float2 dg = mul2(cc, hp[j]);
+        *dx = mul2(lam, be[i]);
+        *db = lx;
+        if (SCALE != kScaleNone) {
+          const float2 q = make_float2(input_scale_slope<SCALE>(al[j].x, f[j].x),
+                                       input_scale_slope<SCALE>(al[j].y, f[j].y));
+          dg = fma2(mul2(lx, be[i]), q, dg);
+          *dx = mul2(*dx, f[j]);
+          *db = mul2(*db, f[j]);
+        }
+        *da = dg;
+        if (!GIVEN) {
+          if (p.b) *db = mul2(mul2(*db, be[i]), write_gate_rest(get2(st.b + el), be[i]));
+          *da = mul2(dg, slope[i]);
+          tb = add2(tb, *da);
+          // dg log2(e) times e, which is -inf where alpha = 0
+          tA = fma2(dg, make_float2(fmaxf(e[i].x, -3e38f), fmaxf(e[i].y, -3e38f)), tA);
+        }
+      };
+      float2 dx, da, db;
+      if (n == kTileT && cols > 1 && vec) {
+#pragma unroll
+        for (int j = kGroup - 1; j >= 0; --j) {
+          token(j, &dx, &da, &db);
+          put2(odx.at(i0 + j), dx);
+          put2(oda.at(i0 + j), da);
+          if (p.b) put2(odb.at(i0 + j), db);
+        }
+      } else {
+#pragma unroll
+        for (int j = kGroup - 1; j >= 0; --j) {
+          if (first + i0 + j >= n) continue;
+          token(j, &dx, &da, &db);
+          put2(odx.at(i0 + j), dx, cols);
+          put2(oda.at(i0 + j), da, cols);
+          if (p.b) put2(odb.at(i0 + j), db, cols);
+        }
       }
     }
-    if (at.warp == 0) carry_rest<SPLIT, true>(ch, k.rank, round, folds, &carry);
+    if (at.warp == 0) carry_rest<SPLIT, CLUSTER, true>(ch, k.rank, round, folds, &carry);
     odx.advance(-step);
     oda.advance(-step);
     odb.advance(-step);
@@ -285,13 +289,13 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
         write2(p.dA_log, 0, c, p.D, vA);
         write2(p.ddt_bias, 0, c, p.D, vb);
       } else {
-        float2* to = sums + ((long long)k.row * ch.cs + k.rank) * p.D + c;
+        float2* to = sums + ((long long)k.row * cs + k.rank) * p.D + c;
         if (cols > 0) to[0] = make_float2(vA.x, vb.x);
         if (cols > 1) to[1] = make_float2(vA.y, vb.y);
       }
     }
   }
-  carry_end(ch);
+  carry_end<CLUSTER>();
 }
 
 // dA_log and ddt_bias: a channel's sums of all blocks, in a fixed order (32 rows of threads,
@@ -331,16 +335,21 @@ struct BwdRun {
     using TD = typename Wide<TX, WIDE>::type;
     using TDG = typename Wide<TD, GIVEN>::type;
     static KernelSlots known[3];
-    const auto k1 = linrec_bwd_kernel<TX, TG, GIVEN, SCALE, TD, TDG, 1>;
-    const auto k2 = linrec_bwd_kernel<TX, TG, GIVEN, SCALE, TD, TDG, 2>;
-    const auto k4 = linrec_bwd_kernel<TX, TG, GIVEN, SCALE, TD, TDG, 4>;
+    using Kernel = void (*)(LinrecArgs, Chains, int, LinrecMaps, const float*, float2*);
+    const ChainKernel<Kernel> ks[3] = {
+        {linrec_bwd_kernel<TX, TG, GIVEN, SCALE, TD, TDG, 1, false>,
+         linrec_bwd_kernel<TX, TG, GIVEN, SCALE, TD, TDG, 1, true>},
+        {linrec_bwd_kernel<TX, TG, GIVEN, SCALE, TD, TDG, 2, false>,
+         linrec_bwd_kernel<TX, TG, GIVEN, SCALE, TD, TDG, 2, true>},
+        {linrec_bwd_kernel<TX, TG, GIVEN, SCALE, TD, TDG, 4, false>,
+         linrec_bwd_kernel<TX, TG, GIVEN, SCALE, TD, TDG, 4, true>}};
     Split sp;
     constexpr size_t smem = sizeof(BwdSmem<TX, TG, TD>);
-    cudaError_t e = choose_split(p, k1, k2, k4, smem, smem, known, &sp);
+    cudaError_t e = choose_split(p, ks, smem, smem, known, &sp);
     if (e != cudaSuccess) return e;
-    return sp.split == 4   ? launch<TX, TG, GIVEN, TD, TDG, 4>(k4, sp.cs)
-           : sp.split == 2 ? launch<TX, TG, GIVEN, TD, TDG, 2>(k2, sp.cs)
-                           : launch<TX, TG, GIVEN, TD, TDG, 1>(k1, sp.cs);
+    return sp.split == 4   ? launch<TX, TG, GIVEN, TD, TDG, 4>(ks[2].of(sp.cs), sp.cs)
+           : sp.split == 2 ? launch<TX, TG, GIVEN, TD, TDG, 2>(ks[1].of(sp.cs), sp.cs)
+                           : launch<TX, TG, GIVEN, TD, TDG, 1>(ks[0].of(sp.cs), sp.cs);
   }
   template <typename TX, typename TG, bool GIVEN, typename TD, typename TDG, int SPLIT, typename K>
   cudaError_t launch(K kernel, int cs) const {

@@ -59,10 +59,17 @@ inline int most_blocks(const LinrecArgs& p) {
 struct KernelSlots {
   std::atomic<int> at[64][kMaxCluster + 1];
 };
+// A shape's kernels: of blocks that are alone on their chains (nothing of the exchange in their
+// registers), and of clusters.
+template <typename K>
+struct ChainKernel {
+  K alone, cluster;
+  K of(int cs) const { return cs > 1 ? cluster : alone; }
+};
 // smem: of the call; most_smem: the most that any call of the kernel takes (its limit is set to
 // that once and for all), both without the cluster's folds.
 template <typename K>
-cudaError_t kernel_slots(K kernel, size_t smem, size_t most_smem, KernelSlots* known,
+cudaError_t kernel_slots(const ChainKernel<K>& k, size_t smem, size_t most_smem, KernelSlots* known,
                          const std::atomic<int>** slots) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -75,11 +82,13 @@ cudaError_t kernel_slots(K kernel, size_t smem, size_t most_smem, KernelSlots* k
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const size_t most = most_smem + 2 * kMaxCluster * sizeof(FoldRow);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+    e = cudaFuncSetAttribute(k.alone, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    e = cudaFuncSetAttribute(k.cluster, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
   if (e == cudaSuccess)
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kLinrecThreads, smem);
+    e = cudaFuncSetAttribute(k.cluster, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess)
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, k.alone, kLinrecThreads, smem);
   if (e != cudaSuccess) return e;
   for (int cs = 2; cs <= kMaxCluster; ++cs) {
     cudaLaunchAttribute attr[1];
@@ -94,7 +103,7 @@ cudaError_t kernel_slots(K kernel, size_t smem, size_t most_smem, KernelSlots* k
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+    e = cudaOccupancyMaxActiveClusters(&n, k.cluster, &cfg);
     if (e != cudaSuccess) return e;
     at[cs].store(n, std::memory_order_relaxed);
   }
@@ -119,8 +128,8 @@ inline long long chains_of(const LinrecArgs& p, int split) {
 //   131072 x 1024                 1x16 444, 2x8 356, 4x8 296 (taken), 4x16 610 (two waves)
 //   8192 x 4096                   1x1 212, 1x4 87, 1x6 80, 2x3 80 (taken), 4x1 84
 template <typename K>
-cudaError_t choose_split(const LinrecArgs& p, K k1, K k2, K k4, size_t smem, size_t most_smem,
-                         KernelSlots* known, Split* out) {
+cudaError_t choose_split(const LinrecArgs& p, const ChainKernel<K> (&ks)[3], size_t smem,
+                         size_t most_smem, KernelSlots* known, Split* out) {
   *out = Split{1, 1};
   const long long chunks = (longest(p) + kLinrecChunk - 1) / kLinrecChunk;
   const long long mean = p.cu ? linrec_chunks(p.cu, p.B, p.T) / p.B : chunks;
@@ -129,7 +138,7 @@ cudaError_t choose_split(const LinrecArgs& p, K k1, K k2, K k4, size_t smem, siz
     const int split = 1 << j;
     if (j > 0 && mean < split) break;  // tiles of more chunks than a sequence has
     const std::atomic<int>* slots = nullptr;
-    cudaError_t e = kernel_slots(j == 0 ? k1 : j == 1 ? k2 : k4, smem, most_smem, known + j, &slots);
+    cudaError_t e = kernel_slots(ks[j], smem, most_smem, known + j, &slots);
     if (e != cudaSuccess) return e;
     const long long n = chains_of(p, split), tiles = (chunks + split - 1) / split;
     const long long room = slots[1].load(std::memory_order_relaxed);

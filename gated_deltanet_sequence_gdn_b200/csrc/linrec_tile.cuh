@@ -90,11 +90,11 @@ struct Chain {
   int row, c0;     // sequence, first channel
   int chunks, tiles, rank;
 };
-template <int SPLIT>
+template <int SPLIT, bool CLUSTER>
 __device__ __forceinline__ Chain chain_of(const LinrecArgs& p, const Chains& ch) {
   Chain k;
-  const int id = blockIdx.x / ch.cs;
-  k.rank = blockIdx.x % ch.cs;
+  const int cs = CLUSTER ? ch.cs : 1, id = blockIdx.x / cs;
+  k.rank = blockIdx.x % cs;
   k.row = id / ch.nblk;
   k.c0 = (id - k.row * ch.nblk) * Shape<SPLIT>::kC;
   if (ch.tab.cu != nullptr) k.row = ch.tab.order[k.row];
@@ -175,18 +175,14 @@ __device__ __forceinline__ float2 carry_through(const FoldRow* row, int r0, int 
 // tile.  Returns what enters that chunk and moves `carry` behind this block's tile; carry_rest
 // moves it behind the round's other tiles, when nobody waits for it any more.  `lost`: a wait
 // has expired, later ones are not tried.
-template <int SPLIT, bool BACK>
+template <int SPLIT, bool CLUSTER, bool BACK>
 __device__ __forceinline__ float2 carry_round(const Chains& ch, int rank, int round, float4 own,
                                               CarrySmem& sm, FoldRow* folds, float2* carry,
                                               bool* lost) {
   float2 in = *carry;
-  if (SPLIT == 1 && ch.cs == 1) {
-    *carry = fma2(first2(own), in, last2(own));
-    return in;
-  }
   const int lane = threadIdx.x & 31, buf = round & 1;
-  FoldRow* row = folds + buf * ch.cs;
-  if (ch.cs > 1) {
+  FoldRow* row = folds + (CLUSTER ? buf * ch.cs : buf);
+  if (CLUSTER) {
     // Once a wait has expired its phase stays open: nothing is armed on it again (an arrival in
     // a phase that expects none is undefined), nothing sent, nothing waited for.
     if (!*lost) {
@@ -204,33 +200,35 @@ __device__ __forceinline__ float2 carry_round(const Chains& ch, int rank, int ro
     row[0][lane] = own;
     __syncwarp();
   }
-  const float2 v = carry_through<SPLIT, BACK>(row, 0, rank, in, nullptr);
+  const float2 v = CLUSTER ? carry_through<SPLIT, BACK>(row, 0, rank, in, nullptr) : in;
   *carry = carry_through<SPLIT, BACK>(row, rank, rank + 1, v, &in);
   return in;
 }
-template <int SPLIT, bool BACK>
+template <int SPLIT, bool CLUSTER, bool BACK>
 __device__ __forceinline__ void carry_rest(const Chains& ch, int rank, int round,
                                            const FoldRow* folds, float2* carry) {
-  if (ch.cs > 1)
+  if (CLUSTER)
     *carry = carry_through<SPLIT, BACK>(folds + (round & 1) * ch.cs, rank + 1, ch.cs, *carry,
                                         nullptr);
 }
 
-__device__ __forceinline__ void carry_begin(const Chains& ch, CarrySmem& sm) {
+template <bool CLUSTER>
+__device__ __forceinline__ void carry_begin(CarrySmem& sm) {
   if (threadIdx.x == 0) {
-    tc::mbar_init(&sm.full[0], 1);
-    tc::mbar_init(&sm.full[1], 1);
-    tc::mbar_init(&sm.loaded[0], 1);
-    tc::mbar_init(&sm.loaded[1], 1);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&sm.full[i], 1);
+      tc::mbar_init(&sm.loaded[i], 1);
+    }
     tc::fence_mbar_init();
   }
   __syncthreads();
-  if (ch.cs > 1) tc::cluster_sync();  // the barriers are there before a peer counts on them
+  if (CLUSTER) tc::cluster_sync();  // the barriers are there before a peer counts on them
 }
 // No block leaves while a peer may still send to it.
-__device__ __forceinline__ void carry_end(const Chains& ch) {
+template <bool CLUSTER>
+__device__ __forceinline__ void carry_end() {
   __syncwarp();
-  if (ch.cs > 1) tc::cluster_sync();
+  if (CLUSTER) tc::cluster_sync();
 }
 
 // Tiles of one tensor to shared memory [tokens][channels].  Tensors whose rows start on 16 bytes come
