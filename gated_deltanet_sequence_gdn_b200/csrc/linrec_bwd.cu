@@ -4,7 +4,19 @@
 //   dx = lambda f beta,  dbeta = lambda f x,  dg = alpha lambda h_{t-1} + lambda beta x f'(g),
 // c runs over the tiles from the last to the first as the forward's state does from the
 // first to the last (linrec_tile.cuh).  The states h_{t-1} of a tile are recomputed in
-// float32 from the state before it, which the forward kept.
+// float32 from the state before it, which the forward kept (4 bytes for 64 elements).
+//
+// Two passes over a tile in shared memory.  The first forms the gates and folds both chains,
+// (A, H) and (A, R); the exponents, the slopes of softplus and beta stay in registers (48 of
+// the 128 that two blocks an SM leave).  The second walks the states forward and the gradients
+// back, four tokens at a time: the later four start from the state that the fold of the first
+// four gives.  All eight at once spilled (sqrt(1 - alpha^2), 64 x 512 x 4096: 561 against 500
+// us).  dA_log and ddt_bias are summed by the lanes that hold their channels, rounding errors
+// kept, and joined over the blocks in a fixed order.
+//
+// What bounds it: 65 instructions an element against 14 bytes of bf16, at 55% of the issue
+// slots with 15 warps an SM.  Measured: 64 sequences of 512 x 4096 bf16 424 us, 4.4 TB/s;
+// float32 of 512 x 2048 353 us, 5.3 TB/s; 131072 x 1024 without a write gate 455 us, 3.0 TB/s.
 #include "linrec_launch.cuh"
 
 namespace gdn {

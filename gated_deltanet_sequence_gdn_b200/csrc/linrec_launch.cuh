@@ -124,7 +124,9 @@ inline long long chains_of(const LinrecArgs& p, int split) {
 // smaller last wave, 286 to 341); fewer run in the largest cluster whose launch still runs at
 // once, and the smaller cluster (fewer exchanges) is taken where shapes are equal.  Forward, us
 // by shape (chunks of a tile x blocks of a cluster):
-//   8192 tokens x 12288 channels  1x1 273, 1x2 200, 2x1 191, 4x1 191 (768 blocks), 1x4 206
+//   8192 tokens x 12288 channels  1x1 269, 1x2 209, 2x1 193, 4x1 192 (taken, 768 blocks)
+//   8192 x 8192                   1x1 206, 1x2 170, 2x1 154, 4x1 128 (taken)
+//   43 x 3699 x 14                53 in tiles of 64 channels, 22 of 16 (taken)
 //   131072 x 1024                 1x16 444, 2x8 356, 4x8 296 (taken), 4x16 610 (two waves)
 //   8192 x 4096                   1x1 212, 1x4 87, 1x6 80, 2x3 80 (taken), 4x1 84
 template <typename K>
