@@ -668,9 +668,11 @@ def _here(dev):
 
 def _new(t, dtype):
     """A contiguous tensor of t's shape (the call that does it in the least host time)."""
-    if t.dtype is dtype and t.is_contiguous():
+    if t.dtype is not dtype:
+        return t.new_empty(t.shape, dtype=dtype)
+    if t.is_contiguous():
         return torch.empty_like(t)
-    return t.new_empty(t.shape, dtype=dtype)
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def _like(t, dtype, shape, dev, name):
@@ -755,13 +757,14 @@ def gdn_linrec_bwd_workspace_bytes(B, T, D, cu_seqlens=None, *, states_given=Fal
         GATES_PRECOMPUTED if gates_precomputed else 0))
 
 
-def _workspace(workspace, need, dev):
+def _workspace(workspace, need, like, dev):
     """(tensor to keep, pointer, bytes) of a call's workspace, allocated here when None."""
     if need == 0:
         return None, None, 0
     if workspace is None:
-        workspace = torch.empty(need, device=dev, dtype=torch.uint8)
-    elif workspace.device != dev or not workspace.is_contiguous():
+        workspace = like.new_empty(need, dtype=torch.uint8)
+        return workspace, workspace.data_ptr(), need
+    if workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace: must be contiguous and on {dev}")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
@@ -819,14 +822,14 @@ def gdn_linrec_fwd(x, a, b=None, A_log=None, dt_bias=None, h0=None, *, cu_seqlen
     if want_states or states is not None:
         shape = (gdn_linrec_chunks(B, T, cu), D)
         if states is None:
-            states = torch.empty(shape, device=dev, dtype=f32)
+            states = x.new_empty(shape, dtype=f32)
         want_states = True
         ps = _dense(states, f32, shape, dev, "states")
     else:
         ps = None
     # a dense batch needs none
     need = 0 if cu is None else lib.gdn_linrec_workspace_bytes(cu, B, T, D)
-    keep, ws, ws_bytes = _workspace(workspace, need, dev)
+    keep, ws, ws_bytes = _workspace(workspace, need, x, dev)
     _check(lib.gdn_linrec_fwd(*ins, _dense(h0, f32, (B, D), dev, "h0"), cu, B, T, D, *lds,
                               _dtype_code(x.dtype), flags | (OUT_F32 if out_f32 else 0), ph, ldh,
                               _dense(ht, f32, (B, D), dev, "ht"), ps, ws, ws_bytes,
@@ -860,7 +863,7 @@ def gdn_linrec_bwd(x, a, b, A_log, dt_bias, h0, dh, dht=None, *, cu_seqlens=None
         ps = _dense(states, f32, (gdn_linrec_chunks(B, T, cu), D), dev, "states")
     keep, ws, ws_bytes = _workspace(
         workspace, lib.gdn_linrec_bwd_workspace_bytes(cu, B, T, D, int(states is not None), flags),
-        dev)
+        x, dev)
     ptr = {k: None if v is None else v.data_ptr() for k, v in out.items()}
     _check(lib.gdn_linrec_bwd(*ins, _dense(h0, f32, (B, D), dev, "h0"), cu, B, T, D, *lds, pdh,
                               lddh, _dense(dht, f32, (B, D), dev, "dht"), ps,
@@ -987,7 +990,7 @@ def _rope_bwd(_, q, k, positions, inv_freq, q_weight, k_weight, dq_out, dk_out, 
     need = 0
     if q_weight is not None or k_weight is not None:
         need = lib.gdn_qk_norm_rope_bwd_workspace_bytes(tokens, Hq, Hk, d, flags)
-    keep, ws, ws_bytes = _workspace(workspace, need, dev)
+    keep, ws, ws_bytes = _workspace(workspace, need, q if q is not None else k, dev)
     ptr = {n: None if v is None else v.data_ptr() for n, v in out.items()}
     _check(lib.gdn_qk_norm_rope_bwd(*args, *gq, *gk, _dtype_code(dt),
                                     flags | (GRAD_F32 if grad_f32 else 0), eps, scale,
@@ -1012,5 +1015,6 @@ def gdn_status(stream=None) -> int:
 def gdn_test_set_wait_fault(site: int, spin_limit: int = 0):
     """Test hook: make the tensor-core chunk kernels leave one bounded wait to
     expire (site 1: the scan's first state hand-off, site 2: the prep's K / Q
-    tiles, site 3: the chunk results in a cluster of the linear recurrence; 0: none), with spin_limit polls per wait (0 = the default)."""
+    tiles, site 3: the chunk results in a cluster of the linear recurrence;
+    0: none), with spin_limit polls per wait (0 = the default)."""
     _check(lib.gdn_test_set_wait_fault(int(site), int(spin_limit)), "gdn_test_set_wait_fault")

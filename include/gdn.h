@@ -502,8 +502,9 @@ size_t gdn2_chunk_workspace_bytes(int B, int T, int H, int dk, int dv, int dtype
  *              Calls that may run at the same time need a workspace each.
  *   Every pointer needs its element alignment only (inputs whose rows are all 16-byte
  *   aligned come by TMA).  At most 2^30 tokens, D and every ld at most 2^21, and fewer
- *   than 2^30 pairs of a chunk and 16 channels: else GDN_ERR_UNSUPPORTED.  States and sums are float32, outputs rounded once; the result
- *   does not depend on how the work was split.  T = 0 and empty sequences copy h0 to ht
+ *   than 2^30 pairs of a chunk and 16 channels: else GDN_ERR_UNSUPPORTED.  States and
+ *   sums are float32, outputs rounded once; the result does not depend on how the work
+ *   was split.  T = 0 and empty sequences copy h0 to ht
  *   (or zeros).  Long sequences of few channels are taken by clusters of thread blocks
  *   that wait for one another, with a limit: an expired wait is reported by
  *   gdn_check_status.
