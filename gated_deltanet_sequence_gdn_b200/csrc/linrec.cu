@@ -170,8 +170,9 @@ linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
       H = both(0.f);
 #pragma unroll 4
       for (int w = 0; w < 8; ++w) {
-        carry_sm.start[at.group(w)] = v;
         const float4 f = carry_sm.fold[at.group(w)];
+        // in the fold's place: 2 KB that let clusters of 2 and 3 keep four blocks an SM
+        put2(&carry_sm.fold[at.group(w)].x, v);
         v = fma2(first2(f), v, last2(f));
         H = fma2(first2(f), H, last2(f));
         A = mul2(A, first2(f));
@@ -181,7 +182,7 @@ linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
     }
     __syncthreads();
     if (p.h) {
-      float2 h = carry_sm.start[threadIdx.x];
+      float2 h = get2(&carry_sm.fold[threadIdx.x].x);
       if (n == kTileT && cols > 1 && vec) {
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {

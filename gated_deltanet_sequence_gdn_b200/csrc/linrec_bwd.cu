@@ -35,7 +35,8 @@ struct BwdSmem {
   static constexpr int kStages = sizeof(BwdStage<TX, TG, TD>) <= 48 * 1024 ? 2 : 1;
   BwdStage<TX, TG, TD> stage[kStages];
   CarrySmem carry;
-  float2 back[kLinrecThreads];  // R of each thread's tokens: c_out = A c_in + R
+  float2 start[kLinrecThreads];  // the state that enters each thread's tokens
+  float2 back[kLinrecThreads];   // R of each thread's tokens: c_out = A c_in + R
   float4 sums[kLinrecThreads];
 };
 
@@ -193,7 +194,7 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
       if (!alone) hnext = state(tt - cs);
 #pragma unroll 4
       for (int w = 0; w < 8; ++w) {
-        sm.carry.start[at.group(w)] = hs;
+        sm.start[at.group(w)] = hs;
         const float4 q = sm.carry.fold[at.group(w)];
         hs = fma2(first2(q), hs, last2(q));
       }
@@ -215,7 +216,7 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
       if (alone) carry = fma2(A, carry, R);
     }
     __syncthreads();
-    hs = sm.carry.start[threadIdx.x];
+    hs = sm.start[threadIdx.x];
     float2 cc = sm.back[threadIdx.x];
     float2 tA = both(0.f), tb = both(0.f);
     // The later group of tokens first; its states from the one in front of it.

@@ -115,8 +115,7 @@ __device__ __forceinline__ Chain chain_of(const LinrecArgs& p, const Chains& ch)
 // Shared memory of the carry: each warp's fold, the carry into the tile, and behind the
 // kernel's own shared memory the cluster's folds, [2 rounds][cs][32].
 struct CarrySmem {
-  float4 fold[kLinrecThreads];   // (A, A', H, H') of each thread's two channels
-  float2 start[kLinrecThreads];  // what enters its tokens
+  float4 fold[kLinrecThreads];  // (A, A', H, H') of each thread's two channels
   uint64_t full[2];          // the round's folds have arrived
   uint64_t loaded[2];        // the stage's tiles have
 };
