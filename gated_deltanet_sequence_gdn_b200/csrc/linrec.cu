@@ -61,6 +61,7 @@ linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
   };
   constexpr int kTileT = Shape<SPLIT>::kT, kC = Shape<SPLIT>::kC, kTileChunks = kTileT / kLinrecChunk;
   const Spot<SPLIT> at;
+  wait_for_launch();
   const Chain k = chain_of<SPLIT, CLUSTER>(p, ch);
   const int c = k.c0 + 2 * at.cl, cols = p.D - c;
   const int cs = CLUSTER ? ch.cs : 1, step = cs * kTileT;
@@ -409,6 +410,7 @@ cudaError_t make_chains(const LinrecArgs& a, void* workspace, cudaStream_t s, Ch
     ch->tab.order = reinterpret_cast<const int*>(ws);
     cudaError_t e = fill_seq_table(a, ch->tab, s);
     if (e != cudaSuccess) return e;
+    ch->after = true;
   }
   ch->status = status_word();
   if (ch->status == nullptr) return cudaErrorUnknown;

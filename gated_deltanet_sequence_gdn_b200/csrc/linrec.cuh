@@ -8,6 +8,29 @@
 
 namespace gdn {
 
+// A kernel that reads what the launch before it wrote, launched while that one still runs: its
+// blocks come in as the other's leave, and wait in wait_for_launch() for the rest of them.
+__device__ __forceinline__ void wait_for_launch() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+inline cudaLaunchAttribute early_launch() {
+  cudaLaunchAttribute a;
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  return a;
+}
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t s, A... args) {
+  cudaLaunchAttribute attr[1] = {early_launch()};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 constexpr int kLinrecChunk = 64;  // tokens of a chunk (GDN_LINREC_CHUNK of the C ABI)
 
 // One batch: B rows of T tokens, or (cu != NULL) B packed sequences over T tokens.

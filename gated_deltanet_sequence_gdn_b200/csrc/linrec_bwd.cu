@@ -58,6 +58,7 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
   FoldRow* folds = reinterpret_cast<FoldRow*>(smem_raw + sizeof(Smem));
   constexpr int kTileT = Shape<SPLIT>::kT, kC = Shape<SPLIT>::kC, kTileChunks = kTileT / kLinrecChunk;
   const Spot<SPLIT> at;
+  wait_for_launch();
   const int first = at.first;
   const Chain k = chain_of<SPLIT, CLUSTER>(p, ch);
   const int c = k.c0 + 2 * at.cl, cols = p.D - c;
@@ -322,6 +323,7 @@ linrec_sums_kernel(const float2* sums, long long rows, int D, float* dA_log, flo
   __shared__ double2 part[kSumRows][33];
   const int c = blockIdx.x * 32 + threadIdx.x;
   double A = 0.0, b = 0.0;
+  wait_for_launch();
   if (c < D)
     for (long long r = threadIdx.y; r < rows; r += kSumRows) {
       const float2 v = sums[r * D + c];
@@ -381,9 +383,8 @@ struct BwdRun {
     cudaError_t e = launch_chains<SPLIT>(kernel, sizeof(BwdSmem<TX, TG, TD>), p, c, cs, vec, s,
                                          maps, states, alone ? nullptr : sums);
     if (e != cudaSuccess || GIVEN || alone) return e;
-    linrec_sums_kernel<<<(p.D + 31) / 32, dim3(32, kSumRows), 0, s>>>(
-        sums, (long long)p.B * cs, p.D, p.dA_log, p.ddt_bias);
-    return cudaGetLastError();
+    return launch_after(linrec_sums_kernel, dim3((p.D + 31) / 32), dim3(32, kSumRows), s, sums,
+                        (long long)p.B * cs, p.D, p.dA_log, p.ddt_bias);
   }
 };
 
@@ -419,6 +420,7 @@ cudaError_t launch_linrec_bwd(const LinrecArgs& a, void* workspace, cudaStream_t
     e = launch_linrec_scan(f, ch, GDN_GRAD_F32, s);
     if (e != cudaSuccess) return e;
     states = f.states_out;
+    ch.after = true;
   }
   return by_type(a, GDN_GRAD_F32, BwdRun{a, ch, states, reinterpret_cast<float2*>(ws), s});
 }

@@ -163,18 +163,22 @@ cudaError_t launch_chains(K kernel, size_t smem, const LinrecArgs& p, const Chai
   Chains ch = chains;
   ch.cs = cs;
   ch.nblk = (p.D + Shape<SPLIT>::kC - 1) / Shape<SPLIT>::kC;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)cs;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  unsigned attrs = 0;
+  if (cs > 1) {
+    attr[attrs].id = cudaLaunchAttributeClusterDimension;
+    attr[attrs].val.clusterDim.x = (unsigned)cs;
+    attr[attrs].val.clusterDim.y = 1;
+    attr[attrs++].val.clusterDim.z = 1;
+  }
+  if (ch.after) attr[attrs++] = early_launch();
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((long long)p.B * ch.nblk * cs));
   cfg.blockDim = dim3(kLinrecThreads);
   cfg.dynamicSmemBytes = smem + (cs > 1 || SPLIT > 1 ? 2 * cs * sizeof(FoldRow) : 0);
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = cs > 1 ? 1 : 0;
+  cfg.numAttrs = attrs;
   return cudaLaunchKernelEx(&cfg, kernel, p, ch, vec, more...);
 }
 

@@ -80,6 +80,7 @@ struct Chains {
   unsigned spin;  // polls before a wait gives up
   bool fault;     // test hook: the first block of a cluster keeps its folds to itself
   bool tma;       // the inputs come by TMA
+  bool after;     // the launch before it is the call's own and writes what this one reads
 };
 
 // One chain, as a block of its cluster sees it.

@@ -134,6 +134,7 @@ qk_rope_bwd_kernel(const __grid_constant__ Sides p, float* partial) {
 __global__ void __launch_bounds__(kThreads)
 qk_rope_sums_kernel(const float* partial, int blocks, int d, float* dqw, float* dkw) {
   const int w = blockIdx.x * kWarps + threadIdx.x / 32, lane = threadIdx.x & 31;
+  wait_for_launch();
   if (w >= 2 * d) return;
   const int side = w >= d, e = w - side * d;
   float* to = side ? dkw : dqw;
@@ -171,9 +172,8 @@ cudaError_t run_bwd(const QkRopeArgs& a, float* partial, cudaStream_t s) {
   cudaError_t e =
       by_size(p, vec_ok(p, sizeof(T), sizeof(TG)), BwdRun<T, TG>{p, partial, s});
   if (e != cudaSuccess || partial == nullptr) return e;
-  qk_rope_sums_kernel<<<(2 * p.d + kWarps - 1) / kWarps, kThreads, 0, s>>>(
-      partial, p.blocks, p.d, a.dqw, a.dkw);
-  return cudaGetLastError();
+  return launch_after(qk_rope_sums_kernel, dim3((2 * p.d + kWarps - 1) / kWarps), dim3(kThreads),
+                      s, partial, p.blocks, p.d, a.dqw, a.dkw);
 }
 
 }  // namespace
