@@ -124,11 +124,12 @@ inline long long chains_of(const LinrecArgs& p, int split) {
 // smaller last wave, 286 to 341); fewer run in the largest cluster whose launch still runs at
 // once, and the smaller cluster (fewer exchanges) is taken where shapes are equal.  Forward, us
 // by shape (chunks of a tile x blocks of a cluster):
-//   8192 tokens x 12288 channels  1x1 269, 1x2 209, 2x1 193, 4x1 192 (taken, 768 blocks)
-//   8192 x 8192                   1x1 206, 1x2 170, 2x1 154, 4x1 128 (taken)
+//   8192 tokens x 12288 channels  1x2 200, 1x3 224, 2x1 185, 2x2 192, 4x1 183 (taken, 768 blocks)
+//   8192 x 8192                   1x3 143, 2x2 129, 4x1 123 (taken)
+//   8192 x 4096                   1x6 80, 2x3 80, 4x1 80, 4x2 78 (taken)
+//   32768 x 2048                  1x8 174, 2x6 153, 4x3 166 (taken), 4x6 178
+//   131072 x 1024, tied           1x16 440, 2x8 363, 4x6 319, 4x8 297 (taken), 4x16 393 (two waves)
 //   43 x 3699 x 14                53 in tiles of 64 channels, 22 of 16 (taken)
-//   131072 x 1024                 1x16 444, 2x8 356, 4x8 296 (taken), 4x16 610 (two waves)
-//   8192 x 4096                   1x1 212, 1x4 87, 1x6 80, 2x3 80 (taken), 4x1 84
 template <typename K>
 cudaError_t choose_split(const LinrecArgs& p, const ChainKernel<K> (&ks)[3], size_t smem,
                          size_t most_smem, KernelSlots* known, Split* out) {

@@ -5,8 +5,8 @@
 //
 // What bounds it: 25 instructions an element against 6 bytes of bf16 (the time of 33), at 55% of
 // the issue slots with the 15 warps an SM that 123 registers leave.  Measured, 16 + 16 heads of
-// 128, bf16, with the launch that joins the weights' gradients: 8192 tokens 54 us, 3.7 TB/s;
-// 65536 tokens 329 us, 4.9 TB/s.  Three blocks an SM spill (69 against 61 us at the time).
+// 128, bf16, with the launch that joins the weights' gradients: 8192 tokens 53 us, 3.8 TB/s;
+// 65536 tokens 328 us, 4.9 TB/s.  Three blocks an SM spill (69 against 61 us at the time).
 #include "qk_rope.cuh"
 
 namespace gdn {
