@@ -10,7 +10,8 @@
 // the HBM alone.  Measured: 64 sequences of 512 x 4096 bf16 179 us, 6.0 TB/s (copy: 6.6);
 // float32 of 512 x 2048 160 us, 6.7 TB/s.  Where there are few chains, their blocks do not
 // share evenly among the SMs and wait more for their own carry: one sequence of 8192 x 12288
-// 182 us, 4.4 TB/s; 131072 x 1024, tied, without a write gate (6 bytes) in clusters 297 us, 2.7 TB/s.
+// 182 us, 4.4 TB/s; 131072 x 1024, tied, without a write gate (6 bytes), in clusters 285 us,
+// 2.8 TB/s.
 //
 // Three barriers a tile: the stage is there; the folds are; the start states are.  One warp
 // joins the folds while the others wait.  Every warp finding its own start state takes one

@@ -128,7 +128,7 @@ inline long long chains_of(const LinrecArgs& p, int split) {
 //   8192 x 8192                   1x3 143, 2x2 129, 4x1 123 (taken)
 //   8192 x 4096                   1x6 80, 2x3 80, 4x1 80, 4x2 78 (taken)
 //   32768 x 2048                  1x8 174, 2x6 153, 4x3 166 (taken), 4x6 178
-//   131072 x 1024, tied           1x16 440, 2x8 363, 4x6 319, 4x8 297 (taken), 4x16 393 (two waves)
+//   131072 x 1024, tied           1x16 440, 2x8 363, 4x6 319, 4x8 297 (taken, 284 by now)
 //   43 x 3699 x 14                53 in tiles of 64 channels, 22 of 16 (taken)
 template <typename K>
 cudaError_t choose_split(const LinrecArgs& p, const ChainKernel<K> (&ks)[3], size_t smem,
