@@ -60,7 +60,8 @@ linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
     TG* a = reinterpret_cast<TG*>(s + kTile * sizeof(TX));
     return FwdStage<TX, TG>{reinterpret_cast<TX*>(s), a, a + kTile};
   };
-  constexpr int kTileT = Shape<SPLIT>::kT, kC = Shape<SPLIT>::kC, kTileChunks = kTileT / kLinrecChunk;
+  constexpr int kTileT = Shape<SPLIT>::kT, kC = Shape<SPLIT>::kC;
+  constexpr int kTileChunks = kTileT / kLinrecChunk;
   const Spot<SPLIT> at;
   wait_for_launch();
   const Chain k = chain_of<SPLIT, CLUSTER>(p, ch);

@@ -47,7 +47,8 @@ __device__ __forceinline__ void add_kept(float2* sum, float2* err, float2 v) {
   *sum = t;
 }
 
-template <typename TX, typename TG, bool GIVEN, int SCALE, typename TD, typename TDG, int SPLIT, bool CLUSTER>
+template <typename TX, typename TG, bool GIVEN, int SCALE, typename TD, typename TDG, int SPLIT,
+          bool CLUSTER>
 __global__ void __launch_bounds__(kLinrecThreads, 2)
 linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ LinrecMaps maps,
                   const float* states, float2* sums) {
@@ -56,7 +57,8 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
   constexpr int kStages = Smem::kStages;
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
   FoldRow* folds = reinterpret_cast<FoldRow*>(smem_raw + sizeof(Smem));
-  constexpr int kTileT = Shape<SPLIT>::kT, kC = Shape<SPLIT>::kC, kTileChunks = kTileT / kLinrecChunk;
+  constexpr int kTileT = Shape<SPLIT>::kT, kC = Shape<SPLIT>::kC;
+  constexpr int kTileChunks = kTileT / kLinrecChunk;
   const Spot<SPLIT> at;
   wait_for_launch();
   const int first = at.first;

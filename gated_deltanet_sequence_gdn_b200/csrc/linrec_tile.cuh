@@ -113,12 +113,12 @@ __device__ __forceinline__ Chain chain_of(const LinrecArgs& p, const Chains& ch)
   return k;
 }
 
-// Shared memory of the carry: each warp's fold, the carry into the tile, and behind the
-// kernel's own shared memory the cluster's folds, [2 rounds][cs][32].
+// Shared memory of the carry: each thread's fold, and behind the kernel's own shared memory
+// the cluster's folds, [2 rounds][cs][32].
 struct CarrySmem {
   float4 fold[kLinrecThreads];  // (A, A', H, H') of each thread's two channels
-  uint64_t full[2];          // the round's folds have arrived
-  uint64_t loaded[2];        // the stage's tiles have
+  uint64_t full[2];             // the round's folds have arrived
+  uint64_t loaded[2];           // the stage's tiles have
 };
 using FoldRow = float4[32];
 
@@ -231,8 +231,8 @@ __device__ __forceinline__ void carry_end() {
   if (CLUSTER) tc::cluster_sync();
 }
 
-// Tiles of one tensor to shared memory [tokens][channels].  Tensors whose rows start on 16 bytes come
-// by TMA, one instruction a tile, through a map over [channels][tokens][rows of the batch]
+// Tiles of one tensor to shared memory [tokens][channels].  Tensors whose rows start on 16 bytes
+// come by TMA, one instruction a tile, through a map over [channels][tokens][rows of the batch]
 // (zeros behind the last token of a dense row and behind the last channel); the tokens behind
 // a packed sequence are the next one's and are cleared by the caller.
 __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, uint64_t* bar, int c0,
