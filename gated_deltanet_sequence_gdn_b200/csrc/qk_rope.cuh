@@ -179,7 +179,7 @@ __device__ __forceinline__ void lane_angles(const Sides& p, const float* cs, con
     take8(sn + k, L.s);
 #pragma unroll
     for (int i = 0; i < 4; ++i) L.s[i] = mul2(L.s[i], sign);
-  } else if (PAIRS == kPairLane) {  // 4 (behind the last one, not used)
+  } else if (PAIRS == kPairLane) {  // 4 (what is behind the last pair is not used: rotate)
     const float sign = back ? 1.f : -1.f;
     const int k = L.turned == 0 ? 0 : L.e0 / 2;
     const float4 c = *reinterpret_cast<const float4*>(cs + k);
@@ -237,7 +237,11 @@ __device__ __forceinline__ void rotate(const Sides& p, const Lane& L, float* swa
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[i] = make_float2(v[2 * i], v[2 * i + 1]);
   }
-  if (p.rot == p.d || L.turned == 8) {  // a whole head's turn needs no look at the lane
+  // A whole head's turn needs no look at the lane, where the head fills its lanes' channels: in a
+  // lane that it ends in, the angles behind the last pair are not there, and 0 (the channels
+  // behind the head) times what the shared memory holds may be NaN, which the backward's sums
+  // would take to the rest of the head.
+  if (L.turned == 8 || (p.rot == p.d && p.d % 8 == 0)) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) y[i] = fma2(o[i], L.s[i], mul2(y[i], L.c[i]));
   } else if (PAIRS != kPairShuffle && L.turned > 0) {
