@@ -795,6 +795,14 @@ def _linrec_sizes(x, cu_seqlens):
     return (cu, n, x.shape[0], x.shape[1]) if cu is not None else (None, *x.shape)
 
 
+def _clear_rest(cu, T, *outs):
+    """Zeros in the tokens behind the last packed sequence, which the library leaves alone."""
+    if cu is not None and cu[-1] < T:
+        for t in outs:
+            if t is not None:
+                t[cu[-1]:].zero_()
+
+
 @_on_device
 def gdn_linrec_fwd(x, a, b=None, A_log=None, dt_bias=None, h0=None, *, cu_seqlens=None,
                    input_scale="none", gates_precomputed=False, out_f32=False, h=None, ht=None,
@@ -807,12 +815,15 @@ def gdn_linrec_fwd(x, a, b=None, A_log=None, dt_bias=None, h0=None, *, cu_seqlen
     With gates_precomputed a is log alpha and b is beta, float32.  A_log, dt_bias [D], h0 [B,D]
     float32.  Returns (h, ht), or (h, ht, states) with want_states: the float32 state before
     each chunk of LINREC_CHUNK tokens [gdn_linrec_chunks(...), D], for gdn_linrec_bwd.  h has
-    the input dtype, or float32 with out_f32, and may be x.  stream: as everywhere."""
+    the input dtype, or float32 with out_f32, and may be x; tokens behind the last packed
+    sequence are zeros in an h that is allocated here, and stay as they are in the caller's.
+    stream: as everywhere."""
     cu, B, T, D = _linrec_sizes(x, cu_seqlens)
     ins, lds, flags = _linrec_inputs(x, a, b, A_log, dt_bias, gates_precomputed, input_scale)
     dev, f32 = x.device, torch.float32
     odt = f32 if out_f32 else x.dtype
-    if h is None:
+    own = h is None
+    if own:
         h = _new(x, odt)
         ph, ldh = h.data_ptr(), D
     else:
@@ -834,6 +845,8 @@ def gdn_linrec_fwd(x, a, b=None, A_log=None, dt_bias=None, h0=None, *, cu_seqlen
                               _dtype_code(x.dtype), flags | (OUT_F32 if out_f32 else 0), ph, ldh,
                               _dense(ht, f32, (B, D), dev, "ht"), ps, ws, ws_bytes,
                               _here(dev)), "gdn_linrec_fwd")
+    if own:
+        _clear_rest(cu, T, h)
     return (h, ht, states) if want_states else (h, ht)
 
 
@@ -846,7 +859,7 @@ def gdn_linrec_bwd(x, a, b, A_log, dt_bias, h0, dh, dht=None, *, cu_seqlens=None
     (None: recomputed here).  Returns a dict: dx, da, db in dh's dtype (da, db float32 with
     gates_precomputed, with respect to log alpha and beta; db None without b), dA_log,
     ddt_bias [D] float32 (None with gates_precomputed), dh0 [B,D] float32 (None unless
-    want_dh0).  Tokens behind the last packed sequence get no value."""
+    want_dh0).  The gradients of tokens behind the last packed sequence are zeros."""
     cu, B, T, D = _linrec_sizes(x, cu_seqlens)
     ins, lds, flags = _linrec_inputs(x, a, b, A_log, dt_bias, gates_precomputed, input_scale)
     dev, f32 = x.device, torch.float32
@@ -871,6 +884,7 @@ def gdn_linrec_bwd(x, a, b, A_log, dt_bias, h0, dh, dht=None, *, cu_seqlens=None
                               ptr["dx"], D, ptr["da"], D, ptr["db"], D, ptr["dA_log"],
                               ptr["ddt_bias"], ptr["dh0"], ws, ws_bytes,
                               _here(dev)), "gdn_linrec_bwd")
+    _clear_rest(cu, T, out["dx"], out["da"], out["db"])
     return out
 
 
