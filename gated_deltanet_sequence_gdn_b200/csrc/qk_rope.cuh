@@ -15,7 +15,8 @@
 // Angles: position * inv_freq in float32 is off by 2^-24 of the angle, which is 0.01 rad
 // at position 10^5.  A turn is held as a 64-bit fraction instead: phase = position *
 // round(2^64 inv_freq / 2 pi) modulo 2^64 is exact but for that one rounding, for every
-// 64-bit position, and its top 32 bits go to sincospi.
+// 64-bit position (off by |position| 2^-65 turns: 2^-22 rad at 2^40), and its top 32 bits go
+// to sincospi.
 #pragma once
 
 #include "common.cuh"
@@ -123,10 +124,17 @@ __device__ __forceinline__ void store8(T* p, int cnt, const float2* f) {
   }
 }
 
-// One turn of inv_freq as a 64-bit fraction.
+// One turn of inv_freq as a 64-bit fraction, rounded once: inv_freq / 2 pi as an unevaluated
+// sum of two doubles (1 / 2 pi is one, to 2^-108), whose whole turns drop out of the larger.
 __device__ __forceinline__ unsigned long long turn_fraction(float inv_freq) {
-  const double t = (double)inv_freq * 0.15915494309189533577;  // 1 / (2 pi)
-  return __double2ull_rz((t - floor(t)) * 18446744073709551616.0);
+  constexpr double kHi = 0.15915494309189534561, kLo = -9.8393383375912434e-18;
+  constexpr double k64 = 18446744073709551616.0;
+  const double f = fabs((double)inv_freq), hi = f * kHi;
+  const double lo = fma(f, kLo, fma(f, kHi, -hi));
+  const double part = (hi - floor(hi)) * k64, whole = floor(part);
+  const unsigned long long turn =
+      __double2ull_rz(whole) + (unsigned long long)__double2ll_rn((part - whole) + lo * k64);
+  return inv_freq < 0.f ? 0 - turn : turn;
 }
 
 // What a lane knows of its 8 channels: cos and the partner's factor +-sin for each, and where

@@ -580,8 +580,9 @@ int gdn_linrec_step(const void* x, const void* a, const void* b, const float* A_
  * scale after that.
  *   q [tokens, Hq, d], k [tokens, Hk, d] dtype, read; heads dense, ldq, ldk elements from
  *     token to token (>= H * d).  Hq or Hk may be 0 (its pointers unused).
- *   positions [tokens] int64 device, any value (the angle is exact for all of them: turns
- *     are 64-bit fractions); inv_freq [rot/2] float32 device; both unused with rot = 0
+ *   positions [tokens] int64 device, any value (a turn is held as a 64-bit fraction, rounded
+ *     once, so that an angle is off by at most |position| 2^-65 turns: 2^-22 rad at 2^40);
+ *     inv_freq [rot/2] float32 device; both unused with rot = 0
  *   q_weight, k_weight [d] float32, or NULL = ones; only with GDN_QK_RMSNORM
  *   d from 1 to 256, rot even, 0 <= rot <= d, 0 <= eps <= 1
  *   q_out, k_out: dtype, ldqo, ldko; written; may be q, k (same ld), must not otherwise
