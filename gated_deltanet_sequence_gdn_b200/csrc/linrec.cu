@@ -203,8 +203,9 @@ linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
     }
     if (at.warp == 0) carry_rest<SPLIT, CLUSTER, false>(ch, k.rank, round, folds, &carry);
   }
-  if (k.rank == 0 && at.warp == 0 && at.part == 0) write2(p.ht, k.row, c, p.D, carry);
   carry_end<CLUSTER>();
+  // ht may be h0, which every block of the cluster has read by now
+  if (k.rank == 0 && at.warp == 0 && at.part == 0) write2(p.ht, k.row, c, p.D, carry);
 }
 
 // The step: HBM-bound on the float32 state, read and written once.  A thread takes 4 channels

@@ -293,7 +293,6 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
       load(round + 1);
     }
   }
-  if (k.rank == 0 && at.warp == 0 && at.part == 0) write2(p.dh0, k.row, c, p.D, carry);
   if (!GIVEN) {
     sm.sums[threadIdx.x] = join4(mul2(sA, both(kLn2)), sb);
     __syncthreads();
@@ -315,6 +314,8 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
     }
   }
   carry_end<CLUSTER>();
+  // dh0 may be dht, which every block of the cluster has read by now
+  if (k.rank == 0 && at.warp == 0 && at.part == 0) write2(p.dh0, k.row, c, p.D, carry);
 }
 
 // dA_log and ddt_bias: a channel's sums of all blocks, in a fixed order (32 rows of threads,

@@ -31,3 +31,38 @@ def test_rows_of_no_sequence_are_zeros(cu, given, dtype):
     mine = torch.full((200, 72), 7.0, device="cuda", dtype=dtype)
     G.gdn_linrec_fwd(*ins(d), h=mine, **kw)  # the caller's own rows stay
     assert (mine[cu[-1]:] == 7.0).all() and torch.equal(mine[:cu[-1]], h[:cu[-1]])
+
+
+def backward_into(d, T, D, dh0):
+    """The C entry point with the caller's dh0; everything else contiguous.  Returns dx."""
+    x = d["x"]
+    B = x.shape[0]
+    code = {F32: G.F32, BF16: G.BF16}[x.dtype]
+    outs = [torch.empty_like(x) for _ in range(3)]
+    sums = [torch.empty(D, device="cuda") for _ in range(2)]
+    need = G.gdn_linrec_bwd_workspace_bytes(B, T, D)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    p = [d[k].data_ptr() for k in ("x", "a", "b", "A_log", "dt_bias", "h0")]
+    st = G.lib.gdn_linrec_bwd(*p, None, B, T, D, D, D, D, d["dh"].data_ptr(), D,
+                              d["dht"].data_ptr(), None, code, 0, outs[0].data_ptr(), D,
+                              outs[1].data_ptr(), D, outs[2].data_ptr(), D, sums[0].data_ptr(),
+                              sums[1].data_ptr(), dh0.data_ptr(), ws.data_ptr(), need,
+                              torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    return outs[0]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,T,D", [(1, 1024, 64), (2, 5000, 40), (3, 200, 600), (1, 4096, 16)])
+def test_final_states_in_the_place_of_the_first(B, T, D, dtype):
+    """ht = h0 and dh0 = dht, where a cluster's blocks all read what one of them writes."""
+    _, d = make(B, T, D, dtype, seed=T)
+    h, ht = G.gdn_linrec_fwd(*ins(d))
+    g = G.gdn_linrec_bwd(*ins(d), d["dh"], d["dht"])
+    for _ in range(20):
+        both = d["h0"].clone()
+        h2, ht2 = G.gdn_linrec_fwd(*ins(dict(d, h0=both)), ht=both)
+        assert ht2 is both and torch.equal(both, ht) and torch.equal(h2, h)
+        both = d["dht"].clone()
+        dx = backward_into(dict(d, dht=both), T, D, both)
+        assert torch.equal(both, g["dh0"]) and torch.equal(dx, g["dx"])
