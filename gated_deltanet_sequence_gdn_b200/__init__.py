@@ -1029,6 +1029,6 @@ def gdn_status(stream=None) -> int:
 def gdn_test_set_wait_fault(site: int, spin_limit: int = 0):
     """Test hook: make the tensor-core chunk kernels leave one bounded wait to
     expire (site 1: the scan's first state hand-off, site 2: the prep's K / Q
-    tiles, site 3: the chunk results in a cluster of the linear recurrence;
-    0: none), with spin_limit polls per wait (0 = the default)."""
+    tiles, site 3: the chunk results in a cluster of the linear recurrence,
+    site 4: its tiles; 0: none), with spin_limit polls per wait (0 = the default)."""
     _check(lib.gdn_test_set_wait_fault(int(site), int(spin_limit)), "gdn_test_set_wait_fault")

@@ -510,7 +510,7 @@ int gdn_check_status(gdn_stream_t stream) {
 }
 
 int gdn_test_set_wait_fault(int site, unsigned spin_limit) {
-  if (site < kFaultNone || site > kFaultLinrec) return GDN_ERR_INVALID_ARG;
+  if (site < kFaultNone || site > kFaultLinrecTiles) return GDN_ERR_INVALID_ARG;
   g_fault_site.store(site);
   g_fault_spin.store(spin_limit == 0 ? kWaitSpin : spin_limit);
   return GDN_OK;

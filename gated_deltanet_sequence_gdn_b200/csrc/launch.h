@@ -79,7 +79,13 @@ int* status_word();
 // bounded wait to expire on purpose, and the poll limit of every bounded wait of
 // the tensor-core chunk kernels (kWaitSpin unless a test lowered it).
 constexpr unsigned kWaitSpin = 1u << 24;
-enum WaitFaultSite { kFaultNone = 0, kFaultScanState = 1, kFaultPrepTiles = 2, kFaultLinrec = 3 };
+enum WaitFaultSite {
+  kFaultNone = 0,
+  kFaultScanState = 1,
+  kFaultPrepTiles = 2,
+  kFaultLinrec = 3,
+  kFaultLinrecTiles = 4
+};
 struct WaitFault {
   int site;
   unsigned spin;

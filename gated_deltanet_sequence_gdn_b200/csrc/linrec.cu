@@ -72,15 +72,16 @@ linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
     const int left = tokens - round * step;
     return left < kTileT ? (left < 0 ? 0 : left) : kTileT;
   };
-  bool late = false;  // a tile has not come in time: no more are asked for
+  int late = -1;  // the round whose tiles have not come in time: no more are asked for
   auto load = [&](int round) {
     const int n = length(round), t = (round * cs + k.rank) * kTileT;
     const FwdStage<TX, TG> st = stage(round);
     if (ch.tma) {
-      if (n > 0 && threadIdx.x == 0 && !late) {
+      if (n > 0 && threadIdx.x == 0 && late < 0) {
         uint64_t* bar = &carry_sm.loaded[round & 1];
         const int y = ch.tab.cu ? (int)k.tok + t : t, z = ch.tab.cu ? 0 : k.row;
         tc::mbar_arrive_expect_tx(bar, stage_size);
+        if (ch.fault == kFaultLinrecTiles) return;
         tma_load_3d(st.x, &maps.x, bar, k.c0, y, z);
         tma_load_3d(st.a, &maps.a, bar, k.c0, y, z);
         if (p.b) tma_load_3d(st.b, &maps.b, bar, k.c0, y, z);
@@ -108,10 +109,10 @@ linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
     const int n = length(round);
     if (!ch.tma) {
       cp_async_wait<0>();
-    } else if (n > 0 && !late &&
-               !tc::mbar_wait(&carry_sm.loaded[round & 1], (round >> 1) & 1, nullptr, 0)) {
+    } else if (n > 0 && late < 0 &&
+               !tc::mbar_wait(&carry_sm.loaded[round & 1], (round >> 1) & 1, nullptr, 0, ch.spin)) {
       report_timeout(ch.status, 0x4c54);
-      late = true;
+      late = round;
     }
     __syncthreads();  // the stage is complete, the other one free
     if (round + 1 < rounds) load(round + 1);
@@ -203,6 +204,9 @@ linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
     }
     if (at.warp == 0) carry_rest<SPLIT, CLUSTER, false>(ch, k.rank, round, folds, &carry);
   }
+  // no copy is to be on its way when the block leaves: once more, with a limit
+  if (late >= 0 && threadIdx.x == 0)
+    tc::mbar_wait(&carry_sm.loaded[late & 1], (late >> 1) & 1, nullptr, 0, 1u << 20);
   carry_end<CLUSTER>();
   // ht may be h0, which every block of the cluster has read by now
   if (k.rank == 0 && at.warp == 0 && at.part == 0) write2(p.ht, k.row, c, p.D, carry);
@@ -419,7 +423,7 @@ cudaError_t make_chains(const LinrecArgs& a, void* workspace, cudaStream_t s, Ch
   if (ch->status == nullptr) return cudaErrorUnknown;
   const WaitFault wf = wait_fault();
   ch->spin = wf.spin;
-  ch->fault = wf.site == kFaultLinrec;
+  ch->fault = wf.site;
   return cudaSuccess;
 }
 

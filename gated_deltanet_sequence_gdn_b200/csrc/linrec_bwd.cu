@@ -72,16 +72,17 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
   auto length = [&](int round) {  // of the round's tile: only the sequence's last is short
     return tile(round) < 0 ? 0 : round == 0 && tokens < kTileT ? tokens : kTileT;
   };
-  bool late = false;  // a tile has not come in time: no more are asked for
+  int late = -1;  // the round whose tiles have not come in time: no more are asked for
   auto load = [&](int round) {
     const int n = length(round), t = tile(round) * kTileT;
     BwdStage<TX, TG, TD>& st = sm.stage[round % kStages];
     if (ch.tma) {
-      if (n > 0 && threadIdx.x == 0 && !late) {
+      if (n > 0 && threadIdx.x == 0 && late < 0) {
         uint64_t* bar = &sm.carry.loaded[round % kStages];
         const int y = ch.tab.cu ? (int)k.tok + t : t, z = ch.tab.cu ? 0 : k.row;
         tc::mbar_arrive_expect_tx(bar, sizeof(st.x) + sizeof(st.a) + (p.b ? sizeof(st.b) : 0) +
                                            sizeof(st.dh));
+        if (ch.fault == kFaultLinrecTiles) return;
         tma_load_3d(st.x, &maps.x, bar, k.c0, y, z);
         tma_load_3d(st.a, &maps.a, bar, k.c0, y, z);
         if (p.b) tma_load_3d(st.b, &maps.b, bar, k.c0, y, z);
@@ -121,11 +122,11 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
     const int tt = tile(round), n = length(round);
     if (!ch.tma) {
       cp_async_wait<0>();
-    } else if (n > 0 && !late &&
+    } else if (n > 0 && late < 0 &&
                !tc::mbar_wait(&sm.carry.loaded[round % kStages], (round / kStages) & 1, nullptr,
-                              0)) {
+                              0, ch.spin)) {
       report_timeout(ch.status, 0x4c54);
-      late = true;
+      late = round;
     }
     __syncthreads();  // the stage is complete, the other one free
     if (kStages > 1 && round + 1 < rounds) load(round + 1);
@@ -313,6 +314,9 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
       }
     }
   }
+  // no copy is to be on its way when the block leaves: once more, with a limit
+  if (late >= 0 && threadIdx.x == 0)
+    tc::mbar_wait(&sm.carry.loaded[late % kStages], (late / kStages) & 1, nullptr, 0, 1u << 20);
   carry_end<CLUSTER>();
   // dh0 may be dht, which every block of the cluster has read by now
   if (k.rank == 0 && at.warp == 0 && at.part == 0) write2(p.dh0, k.row, c, p.D, carry);

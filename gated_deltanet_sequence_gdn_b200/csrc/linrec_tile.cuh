@@ -78,7 +78,8 @@ struct Chains {
   int cs;    // blocks of a cluster
   int* status;
   unsigned spin;  // polls before a wait gives up
-  bool fault;     // test hook: the first block of a cluster keeps its folds to itself
+  int fault;      // test hook (WaitFaultSite): the first block of a cluster keeps its folds to
+                  // itself, or the tiles' copies are not asked for
   bool tma;       // the inputs come by TMA
   bool after;     // the launch before it is the call's own and writes what this one reads
 };
@@ -189,7 +190,7 @@ __device__ __forceinline__ float2 carry_round(const Chains& ch, int rank, int ro
       if (lane == 0)
         tc::mbar_arrive_expect_tx(&sm.full[buf], (uint32_t)(ch.cs * 32 * sizeof(float4)));
       __syncwarp();
-      if (!(ch.fault && rank == 0))
+      if (!(ch.fault == kFaultLinrec && rank == 0))
         for (int r = 0; r < ch.cs; ++r)
           st_async_peer(tc::map_peer(&row[rank][lane], r), own, tc::map_peer(&sm.full[buf], r));
       const bool ok = tc::mbar_wait(&sm.full[buf], (round >> 1) & 1, nullptr, 0, ch.spin);

@@ -644,7 +644,9 @@ int gdn_check_status(gdn_stream_t stream);
  *           them expires;
  *   site 2: the WY prep withholds its K / Q tile loads;
  *   site 3: the linear recurrence: the first block of a cluster keeps its chunks'
- *           results to itself, so the waits of the others expire.
+ *           results to itself, so the waits of the others expire;
+ *   site 4: the linear recurrence does not ask for its tiles (inputs whose rows are
+ *           16-byte aligned), so the waits for them expire.
  *   spin_limit: polls before a wait gives up, for every bounded wait of those
  *   kernels (0 = the default, 2^24).  The setting is process-wide and stays
  *   until changed; the outputs of a faulted call are not valid.

@@ -66,3 +66,26 @@ def test_final_states_in_the_place_of_the_first(B, T, D, dtype):
         both = d["dht"].clone()
         dx = backward_into(dict(d, dht=both), T, D, both)
         assert torch.equal(both, g["dh0"]) and torch.equal(dx, g["dx"])
+
+
+@pytest.mark.parametrize("B,T,D", [(2, 300, 64), (1, 5000, 64), (300, 200, 128)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_tiles_that_do_not_come_are_reported(B, T, D, dtype):
+    """The tiles' copies are not asked for: the waits for them end and say so, in lone blocks and
+    in clusters, and the next call is right again."""
+    _, d = make(B, T, D, dtype, seed=17)
+    h, ht, st = G.gdn_linrec_fwd(*ins(d), want_states=True)
+    g = G.gdn_linrec_bwd(*ins(d), d["dh"], d["dht"], states=st)
+    assert G.gdn_status() == 0
+    try:
+        G.gdn_test_set_wait_fault(4, 1 << 10)
+        G.gdn_linrec_fwd(*ins(d))
+        assert G.gdn_status() == -4
+        G.gdn_linrec_bwd(*ins(d), d["dh"], d["dht"], states=st)
+        assert G.gdn_status() == -4
+    finally:
+        G.gdn_test_set_wait_fault(0, 0)
+    h2, ht2 = G.gdn_linrec_fwd(*ins(d))
+    g2 = G.gdn_linrec_bwd(*ins(d), d["dh"], d["dht"], states=st)
+    assert torch.equal(h, h2) and torch.equal(ht, ht2)
+    assert all(torch.equal(g[k], g2[k]) for k in g)
