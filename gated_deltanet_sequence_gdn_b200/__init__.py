@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 import os
 
 import torch
@@ -646,18 +647,28 @@ def gdn_rmsnorm_gated(o, z, weight, *, eps=1e-6, y=None, stream=None):
 def _on_device(fn):
     """Runs an entry point on its first argument's device and on `stream` (default: that
     device's current stream); what it allocates then belongs to that stream."""
+    sig = inspect.signature(fn)
+    name = next(iter(sig.parameters))
+
     @functools.wraps(fn)
-    def call(first, *args, stream=None, **kw):
+    def call(*args, stream=None, **kw):
+        first = args[0] if args else kw.get(name)
+        if not isinstance(first, torch.Tensor):
+            raise TypeError(f"{fn.__name__}: {name} must be a tensor")
         index = first.get_device()
         if index < 0:
             raise ValueError("tensor must live on a CUDA device")
         if stream is None and index == torch.cuda.current_device():
-            return fn(first, *args, **kw)
+            return fn(*args, **kw)
         dev = first.device
         if stream is not None and stream.device != dev:
             raise ValueError(f"stream of {stream.device} for tensors of {dev}")
         with torch.cuda.device(dev), torch.cuda.stream(stream):
-            return fn(first, *args, **kw)
+            return fn(*args, **kw)
+
+    if "stream" not in sig.parameters:
+        more = inspect.Parameter("stream", inspect.Parameter.KEYWORD_ONLY, default=None)
+        call.__signature__ = sig.replace(parameters=[*sig.parameters.values(), more])
     return call
 
 

@@ -1,0 +1,29 @@
+"""How the entry points of the gated linear recurrence and of the norm-and-rotation take their
+arguments, without a GPU."""
+import inspect
+
+import pytest
+import torch
+
+import gated_deltanet_sequence_gdn_b200 as G
+
+HERE = torch.zeros(2, 8)
+W = torch.zeros(8)
+
+
+@pytest.mark.parametrize("fn,kw", [
+    (G.gdn_linrec_fwd, dict(x=HERE, a=HERE, A_log=W, dt_bias=W, cu_seqlens=[0, 2])),
+    (G.gdn_linrec_bwd, dict(x=HERE, a=HERE, b=None, A_log=W, dt_bias=W, h0=None, dh=HERE,
+                            cu_seqlens=[0, 2])),
+    (G.gdn_linrec_step, dict(x=HERE, a=HERE, b=None, A_log=W, dt_bias=W, state=HERE)),
+])
+def test_every_argument_has_its_name(fn, kw):
+    """By name all the way: what is wrong with these calls is that the tensors are the host's."""
+    assert list(inspect.signature(fn).parameters)[0] == "x"
+    assert inspect.signature(fn).parameters["stream"].kind is inspect.Parameter.KEYWORD_ONLY
+    with pytest.raises(ValueError, match="CUDA device"):
+        fn(**kw)
+    with pytest.raises(TypeError, match="x must be a tensor"):
+        fn(**dict(kw, x=None))
+    with pytest.raises(TypeError, match="x must be a tensor"):
+        fn(**{k: v for k, v in kw.items() if k != "x"})

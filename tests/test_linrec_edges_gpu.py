@@ -89,3 +89,20 @@ def test_tiles_that_do_not_come_are_reported(B, T, D, dtype):
     g2 = G.gdn_linrec_bwd(*ins(d), d["dh"], d["dht"], states=st)
     assert torch.equal(h, h2) and torch.equal(ht, ht2)
     assert all(torch.equal(g[k], g2[k]) for k in g)
+
+
+def test_every_argument_by_name_and_on_another_stream():
+    s, d = make(2, 70, 40, F32, seed=18)
+    named = {k: d[k] for k in ("x", "a", "b", "A_log", "dt_bias", "h0")}
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    h, ht = G.gdn_linrec_fwd(**named, stream=side)
+    g = G.gdn_linrec_bwd(**named, dh=d["dh"], dht=d["dht"], stream=side)
+    state = d["h0"].clone()
+    side.wait_stream(torch.cuda.current_stream())
+    one = {k: d[k][:, 0] for k in ("x", "a", "b")}
+    h1 = G.gdn_linrec_step(**one, A_log=d["A_log"], dt_bias=d["dt_bias"], state=state, stream=side)
+    torch.cuda.synchronize()
+    P.check("h", h, *P.forward_bounds(*ins(s))["h"])
+    P.check("dx", g["dx"], *P.backward_bounds(*ins(s, "dh", "dht"))["dx"])
+    P.check("first", h1, *(v[:, 0] for v in P.forward_bounds(*ins(s))["h"]))
