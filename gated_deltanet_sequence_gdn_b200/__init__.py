@@ -926,7 +926,7 @@ _NORMS = {None: 0, "none": 0, "l2": QK_L2NORM, "rms": QK_RMSNORM}
 
 def _rope_inputs(q, k, positions, inv_freq, q_weight, k_weight, norm, interleaved):
     """Checked arguments that both entry points share."""
-    some = q if q is not None else k
+    some = _either(q, k)
     dt, dev, lead, d = some.dtype, some.device, some.shape[:-2], some.shape[-1]
     if len(lead) not in (1, 2):
         raise ValueError("q, k: expected [T, H, d] or [B, T, H, d]")
@@ -946,6 +946,13 @@ def _rope_inputs(q, k, positions, inv_freq, q_weight, k_weight, norm, interleave
           for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight"))]
     flags = _NORMS[norm] | (ROPE_INTERLEAVED if interleaved else 0)
     return (pq, pk, pp, pf, *pw, tokens, Hq, Hk, d, rot, ldq, ldk), flags, dt, dev, lead
+
+
+def _either(q, k):
+    """The tensor whose device a call runs on."""
+    if q is None and k is None:
+        raise ValueError("one of q and k must be given")
+    return q if q is not None else k
 
 
 def _rope_out(t, out, dt, dev, name):
@@ -968,7 +975,7 @@ def gdn_qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, *,
     positions [...] (int64) * inv_freq (float32; None: no rotation), in one pass; queries are
     multiplied by scale.  The leading axes are [T] or [B, T]; q and k may be slices of one
     projection's output, and one of them None.  Returns (q_out, k_out), which may be q and k."""
-    return _rope_fwd(q if q is not None else k, q, k, positions, inv_freq, q_weight, k_weight,
+    return _rope_fwd(_either(q, k), q, k, positions, inv_freq, q_weight, k_weight,
                      norm, eps, scale, interleaved, q_out, k_out, stream=stream)
 
 
@@ -995,7 +1002,7 @@ def gdn_qk_norm_rope_bwd(q, k, positions, inv_freq, q_weight, k_weight, dq_out, 
     """Gradients of gdn_qk_norm_rope at its inputs q, k and weights, from those at its outputs
     (the input dtype, or float32 with grad_f32).  Returns a dict: dq, dk in the gradients'
     dtype, dq_weight, dk_weight [d] float32 (None where the weight is)."""
-    return _rope_bwd(q if q is not None else k, q, k, positions, inv_freq, q_weight, k_weight,
+    return _rope_bwd(_either(q, k), q, k, positions, inv_freq, q_weight, k_weight,
                      dq_out, dk_out, norm, eps, scale, interleaved, grad_f32, workspace,
                      stream=stream)
 
@@ -1015,7 +1022,7 @@ def _rope_bwd(_, q, k, positions, inv_freq, q_weight, k_weight, dq_out, dk_out, 
     need = 0
     if q_weight is not None or k_weight is not None:
         need = lib.gdn_qk_norm_rope_bwd_workspace_bytes(tokens, Hq, Hk, d, flags)
-    keep, ws, ws_bytes = _workspace(workspace, need, q if q is not None else k, dev)
+    keep, ws, ws_bytes = _workspace(workspace, need, _either(q, k), dev)
     ptr = {n: None if v is None else v.data_ptr() for n, v in out.items()}
     _check(lib.gdn_qk_norm_rope_bwd(*args, *gq, *gk, _dtype_code(dt),
                                     flags | (GRAD_F32 if grad_f32 else 0), eps, scale,

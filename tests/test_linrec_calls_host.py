@@ -27,3 +27,10 @@ def test_every_argument_has_its_name(fn, kw):
         fn(**dict(kw, x=None))
     with pytest.raises(TypeError, match="x must be a tensor"):
         fn(**{k: v for k, v in kw.items() if k != "x"})
+
+
+@pytest.mark.parametrize("fn,more", [(G.gdn_qk_norm_rope, ()),
+                                     (G.gdn_qk_norm_rope_bwd, (None, None, None, None))])
+def test_neither_q_nor_k(fn, more):
+    with pytest.raises(ValueError, match="q and k"):
+        fn(None, None, torch.zeros(1), None, *more)
