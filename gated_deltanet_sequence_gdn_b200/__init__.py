@@ -756,15 +756,18 @@ def gdn_linrec_chunks(B, T, cu_seqlens=None) -> int:
 
 
 def gdn_linrec_workspace_bytes(B, T, D, cu_seqlens=None) -> int:
-    """Bytes of device workspace gdn_linrec_fwd needs (T: all packed tokens)."""
-    return int(lib.gdn_linrec_workspace_bytes(_host_offsets(cu_seqlens)[0], B, T, D))
+    """Bytes of device workspace gdn_linrec_fwd needs (with cu_seqlens T is all packed tokens
+    and B the offsets' number of sequences, whatever is passed)."""
+    cu, n = _host_offsets(cu_seqlens)
+    return int(lib.gdn_linrec_workspace_bytes(cu, B if cu is None else n, T, D))
 
 
 def gdn_linrec_bwd_workspace_bytes(B, T, D, cu_seqlens=None, *, states_given=False,
                                    gates_precomputed=False) -> int:
-    """Bytes of device workspace gdn_linrec_bwd needs (T: all packed tokens)."""
+    """Bytes of device workspace gdn_linrec_bwd needs (B and T as above)."""
+    cu, n = _host_offsets(cu_seqlens)
     return int(lib.gdn_linrec_bwd_workspace_bytes(
-        _host_offsets(cu_seqlens)[0], B, T, D, int(states_given),
+        cu, B if cu is None else n, T, D, int(states_given),
         GATES_PRECOMPUTED if gates_precomputed else 0))
 
 

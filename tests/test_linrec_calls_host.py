@@ -34,3 +34,14 @@ def test_every_argument_has_its_name(fn, kw):
 def test_neither_q_nor_k(fn, more):
     with pytest.raises(ValueError, match="q and k"):
         fn(None, None, torch.zeros(1), None, *more)
+
+
+def test_workspace_queries_take_the_sequences_from_the_offsets():
+    """Whatever B says: the library reads B + 1 offsets."""
+    cu = list(range(0, 4000, 8))
+    n, T = len(cu) - 1, cu[-1]
+    for B in (0, 1, n, 10 ** 6):
+        assert G.gdn_linrec_workspace_bytes(B, T, 64, cu) == \
+            G.lib.gdn_linrec_workspace_bytes((G._ll * (n + 1))(*cu), n, T, 64) > 0
+        assert G.gdn_linrec_bwd_workspace_bytes(B, T, 64, torch.tensor(cu)) == \
+            G.lib.gdn_linrec_bwd_workspace_bytes((G._ll * (n + 1))(*cu), n, T, 64, 0, 0) > 0
