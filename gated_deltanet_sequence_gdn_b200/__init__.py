@@ -927,14 +927,19 @@ def gdn_linrec_step(x, a, b, A_log, dt_bias, state, *, input_scale="none",
 _NORMS = {None: 0, "none": 0, "l2": QK_L2NORM, "rms": QK_RMSNORM}
 
 
+def _norm_flag(norm):
+    if norm not in _NORMS:
+        raise ValueError(f"norm: expected 'rms', 'l2' or None, got {norm!r}")
+    return _NORMS[norm]
+
+
 def _rope_inputs(q, k, positions, inv_freq, q_weight, k_weight, norm, interleaved):
     """Checked arguments that both entry points share."""
     some = _either(q, k)
     dt, dev, lead, d = some.dtype, some.device, some.shape[:-2], some.shape[-1]
     if len(lead) not in (1, 2):
         raise ValueError("q, k: expected [T, H, d] or [B, T, H, d]")
-    if norm not in _NORMS:
-        raise ValueError(f"norm: expected 'rms', 'l2' or None, got {norm!r}")
+    flags = _norm_flag(norm) | (ROPE_INTERLEAVED if interleaved else 0)
     Hq, Hk = (0 if t is None else t.shape[-2] for t in (q, k))
     tokens = lead.numel()
     pq, ldq = _strided(q, dt, (*lead, Hq, d), dev, "q", 2)
@@ -947,7 +952,6 @@ def _rope_inputs(q, k, positions, inv_freq, q_weight, k_weight, norm, interleave
         pp = _dense(positions, torch.int64, lead, dev, "positions")
     pw = [_dense(w, torch.float32, (d,), dev, n)
           for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight"))]
-    flags = _NORMS[norm] | (ROPE_INTERLEAVED if interleaved else 0)
     return (pq, pk, pp, pf, *pw, tokens, Hq, Hk, d, rot, ldq, ldk), flags, dt, dev, lead
 
 
@@ -996,7 +1000,7 @@ def _rope_fwd(_, q, k, positions, inv_freq, q_weight, k_weight, norm, eps, scale
 
 def gdn_qk_norm_rope_bwd_workspace_bytes(tokens, Hq, Hk, d, norm="rms") -> int:
     """Bytes of device workspace gdn_qk_norm_rope_bwd needs for the weights' gradients."""
-    return int(lib.gdn_qk_norm_rope_bwd_workspace_bytes(tokens, Hq, Hk, d, _NORMS[norm]))
+    return int(lib.gdn_qk_norm_rope_bwd_workspace_bytes(tokens, Hq, Hk, d, _norm_flag(norm)))
 
 
 def gdn_qk_norm_rope_bwd(q, k, positions, inv_freq, q_weight, k_weight, dq_out, dk_out, *,

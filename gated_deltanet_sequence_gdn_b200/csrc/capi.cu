@@ -648,6 +648,8 @@ int gdn_linrec_step(const void* x, const void* a, const void* b, const float* A_
 
 // ---- norm and rotation of q and k ---------------------------------------------------------
 
+constexpr long long kRopeTokens = (1LL << 30) - 1, kRopeHeads = 1 << 20;
+
 static int validate_rope(const QkRopeArgs& p, int more_flags) {
   const int norms = GDN_QK_L2NORM | GDN_QK_RMSNORM;
   if (p.tokens < 0 || p.Hq < 0 || p.Hk < 0 || p.d <= 0 || !ok_dtype(p.dtype))
@@ -661,7 +663,7 @@ static int validate_rope(const QkRopeArgs& p, int more_flags) {
   if (!ok_opt_f32(p.q_weight) || !ok_opt_f32(p.k_weight) || !ok_opt_f32(p.dqw) ||
       !ok_opt_f32(p.dkw))
     return GDN_ERR_INVALID_ARG;
-  if (p.d > 256 || p.Hq + (long long)p.Hk > (1 << 20) || p.tokens > 0x3fffffffLL)
+  if (p.d > 256 || p.Hq + (long long)p.Hk > kRopeHeads || p.tokens > kRopeTokens)
     return GDN_ERR_UNSUPPORTED;
   if (p.tokens == 0 || p.Hq + p.Hk == 0) return GDN_OK;
   const size_t es = elem_size(p.dtype);
@@ -694,7 +696,10 @@ int gdn_qk_norm_rope(const void* q, const void* k, const long long* positions,
 }
 
 size_t gdn_qk_norm_rope_bwd_workspace_bytes(long long tokens, int Hq, int Hk, int d, int flags) {
-  if (tokens <= 0 || Hq < 0 || Hk < 0 || Hq + (long long)Hk == 0 || d <= 0 || d > 256) return 0;
+  const long long heads = Hq + (long long)Hk;
+  if (tokens <= 0 || tokens > kRopeTokens || Hq < 0 || Hk < 0 || heads == 0 ||
+      heads > kRopeHeads || d <= 0 || d > 256)
+    return 0;
   return qk_rope_bwd_workspace_bytes(tokens, Hq, Hk, d, flags);
 }
 

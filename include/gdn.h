@@ -588,7 +588,8 @@ int gdn_linrec_step(const void* x, const void* a, const void* b, const float* A_
  *   q_out, k_out: dtype, ldqo, ldko; written; may be q, k (same ld), must not otherwise
  *     overlap an input
  * float32 arithmetic, outputs rounded once.  Element alignment is enough (rows of whole
- * 16-byte pieces move in them).  At most 2^30 tokens and 2^20 heads.
+ * 16-byte pieces move in them).  Fewer than 2^30 tokens, at most 2^20
+ * heads: else GDN_ERR_UNSUPPORTED.
  */
 int gdn_qk_norm_rope(const void* q, const void* k, const long long* positions,
                      const float* inv_freq, const float* q_weight, const float* k_weight,
@@ -617,7 +618,8 @@ int gdn_qk_norm_rope_bwd(const void* q, const void* k, const long long* position
                          float* dk_weight, void* workspace, size_t ws_bytes,
                          gdn_stream_t stream);
 
-/* Device workspace bytes gdn_qk_norm_rope_bwd needs (0 without GDN_QK_RMSNORM). */
+/* Device workspace bytes gdn_qk_norm_rope_bwd needs (0 without GDN_QK_RMSNORM and for sizes that
+ * the call refuses). */
 size_t gdn_qk_norm_rope_bwd_workspace_bytes(long long tokens, int Hq, int Hk, int d, int flags);
 
 /*

@@ -45,3 +45,13 @@ def test_workspace_queries_take_the_sequences_from_the_offsets():
             G.lib.gdn_linrec_workspace_bytes((G._ll * (n + 1))(*cu), n, T, 64) > 0
         assert G.gdn_linrec_bwd_workspace_bytes(B, T, 64, torch.tensor(cu)) == \
             G.lib.gdn_linrec_bwd_workspace_bytes((G._ll * (n + 1))(*cu), n, T, 64, 0, 0) > 0
+
+
+def test_rotation_workspace_query_of_refused_sizes():
+    query = G.gdn_qk_norm_rope_bwd_workspace_bytes
+    assert query(2 ** 30 - 1, 4, 2, 64) == query(10 ** 6, 4, 2, 64) > 0
+    for sizes in ((2 ** 30, 4, 2, 64), (2 ** 62, 4, 2, 64), (5, 2 ** 20, 1, 64),
+                  (5, 2 ** 31 - 1, 2 ** 31 - 1, 64), (5, 4, 2, 257), (5, 0, 0, 64)):
+        assert query(*sizes) == 0, sizes
+    with pytest.raises(ValueError, match="norm"):
+        query(5, 4, 2, 64, "layer")
