@@ -518,8 +518,11 @@ int gdn_test_set_wait_fault(int site, unsigned spin_limit) {
 
 // ---- gated linear recurrence ------------------------------------------------------------
 
-// The checks the recurrence's calls share; *chunks is set where they pass.
-static int validate_linrec(const LinrecArgs& p, int more_flags, long long* chunks) {
+// The checks the recurrence's calls share; *chunks is set where they pass.  most_ld: the scan and
+// its backward keep 32-bit byte offsets inside a tile of 256 tokens, the step has none.
+constexpr long long kScanLd = 1 << 21, kStepLd = 1LL << 32;
+static int validate_linrec(const LinrecArgs& p, int more_flags, long long most_ld,
+                           long long* chunks) {
   const int scales = GDN_LINREC_TIED | GDN_LINREC_UNIT;
   if (p.B < 0 || p.T < 0 || p.D <= 0 || !ok_dtype(p.dtype)) return GDN_ERR_INVALID_ARG;
   if (p.flags & ~(GDN_GATES_PRECOMPUTED | scales | more_flags)) return GDN_ERR_INVALID_ARG;
@@ -530,11 +533,11 @@ static int validate_linrec(const LinrecArgs& p, int more_flags, long long* chunk
       if (p.cu[i + 1] < p.cu[i]) return GDN_ERR_INVALID_ARG;
   }
   *chunks = linrec_chunks(p.cu, p.B, p.T);
-  // token, chunk and block numbers are 32-bit, and so are byte offsets inside a tile of 256 tokens
+  // token, chunk and block numbers are 32-bit
   const long long blocks = (p.D + 15) / 16;
   if (p.T > 1 << 30 || *chunks * blocks > 0x3fffffffLL || p.B * blocks > 0x3fffffffLL)
     return GDN_ERR_UNSUPPORTED;
-  if (p.ldx > 1 << 21 || p.lda > 1 << 21 || p.ldb > 1 << 21 || p.D > 1 << 21)
+  if (p.ldx > most_ld || p.lda > most_ld || p.ldb > most_ld || p.D > 1 << 21)
     return GDN_ERR_UNSUPPORTED;
   if (p.B == 0 || *chunks == 0) return GDN_OK;
   const size_t es = elem_size(p.dtype), ges = (p.flags & GDN_GATES_PRECOMPUTED) ? 4 : es;
@@ -576,7 +579,7 @@ int gdn_linrec_fwd(const void* x, const void* a, const void* b, const float* A_l
   p.cu = cu_seqlens; p.B = B; p.T = T; p.D = D; p.ldx = ldx; p.lda = lda; p.ldb = ldb;
   p.dtype = dtype; p.flags = flags; p.h = h; p.ldh = ldh; p.ht = ht; p.states_out = states;
   long long chunks = 0;
-  const int st = validate_linrec(p, GDN_OUT_F32, &chunks);
+  const int st = validate_linrec(p, GDN_OUT_F32, kScanLd, &chunks);
   if (st != GDN_OK) return st;
   if (!ok_opt_f32(h0) || !ok_opt_f32(ht) || !ok_opt_f32(states)) return GDN_ERR_INVALID_ARG;
   cudaStream_t s = (cudaStream_t)stream;
@@ -584,7 +587,7 @@ int gdn_linrec_fwd(const void* x, const void* a, const void* b, const float* A_l
   if (chunks == 0) return from_cuda(launch_copy_state(h0, ht, (size_t)B * D, s));
   if (!ok_elem(h, (flags & GDN_OUT_F32) ? 4 : elem_size(dtype)) || ldh < D)
     return GDN_ERR_INVALID_ARG;
-  if (ldh > 1 << 21) return GDN_ERR_UNSUPPORTED;
+  if (ldh > kScanLd) return GDN_ERR_UNSUPPORTED;
   if (!ok_workspace(workspace, ws_bytes, linrec_workspace_bytes(cu_seqlens, B, T, D)))
     return GDN_ERR_WORKSPACE;
   return from_cuda(launch_linrec_fwd(p, workspace, s));
@@ -604,7 +607,7 @@ int gdn_linrec_bwd(const void* x, const void* a, const void* b, const float* A_l
   p.dx = dx; p.lddx = lddx; p.da = da; p.ldda = ldda; p.db = db; p.lddb = lddb;
   p.dA_log = dA_log; p.ddt_bias = ddt_bias; p.dh0 = dh0;
   long long chunks = 0;
-  const int st = validate_linrec(p, GDN_GRAD_F32, &chunks);
+  const int st = validate_linrec(p, GDN_GRAD_F32, kScanLd, &chunks);
   if (st != GDN_OK) return st;
   const bool given = flags & GDN_GATES_PRECOMPUTED;
   if (!ok_opt_f32(h0) || !ok_opt_f32(dht) || !ok_opt_f32(dh0) || !ok_opt_f32(states))
@@ -622,7 +625,7 @@ int gdn_linrec_bwd(const void* x, const void* a, const void* b, const float* A_l
   if (!ok_elem(dh, ds) || lddh < D || !ok_elem(dx, ds) || lddx < D || !ok_elem(da, gs) ||
       ldda < D || (db != nullptr && (!ok_elem(db, gs) || lddb < D)))
     return GDN_ERR_INVALID_ARG;
-  if (lddh > 1 << 21 || lddx > 1 << 21 || ldda > 1 << 21 || lddb > 1 << 21)
+  if (lddh > kScanLd || lddx > kScanLd || ldda > kScanLd || lddb > kScanLd)
     return GDN_ERR_UNSUPPORTED;
   if (!ok_workspace(workspace, ws_bytes,
                     linrec_bwd_workspace_bytes(cu_seqlens, B, T, D, states != nullptr, flags)))
@@ -639,10 +642,11 @@ int gdn_linrec_step(const void* x, const void* a, const void* b, const float* A_
   p.B = N; p.T = 1; p.D = D; p.ldx = ldx; p.lda = lda; p.ldb = ldb;
   p.dtype = dtype; p.flags = flags; p.h = h; p.ldh = ldh;
   long long chunks = 0;
-  const int st = validate_linrec(p, GDN_OUT_F32, &chunks);
+  const int st = validate_linrec(p, GDN_OUT_F32, kStepLd, &chunks);
   if (st != GDN_OK || N == 0) return st;
   if (!ok_elem(state, 4) || !ok_elem(h, (flags & GDN_OUT_F32) ? 4 : elem_size(dtype)) || ldh < D)
     return GDN_ERR_INVALID_ARG;
+  if (ldh > kStepLd) return GDN_ERR_UNSUPPORTED;
   return from_cuda(launch_linrec_step(p, state, (cudaStream_t)stream));
 }
 

@@ -557,7 +557,8 @@ size_t gdn_linrec_bwd_workspace_bytes(const long long* cu_seqlens, int B, int T,
  * gdn_linrec_step -- one token of the gated linear recurrence for N sequences: the decode
  * step beside gdn_recurrent_step, the same gates and input scale as gdn_linrec_fwd.
  *   x, a, b [N, D] dtype (a, b float32 g, beta with GDN_GATES_PRECOMPUTED; b NULL: beta
- *     = 1), ldx, lda, ldb elements from one sequence to the next
+ *     = 1), ldx, lda, ldb elements from one sequence to the next (up to 2^32, so that one
+ *     token of a [N, T, D] batch is read where it is)
  *   state   [N, D] float32, read and updated in place
  *   h       [N, D] dtype (float32 with GDN_OUT_F32), ldh, written; may be x
  *   flags   as for gdn_linrec_fwd

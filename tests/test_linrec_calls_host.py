@@ -55,3 +55,15 @@ def test_rotation_workspace_query_of_refused_sizes():
         assert query(*sizes) == 0, sizes
     with pytest.raises(ValueError, match="norm"):
         query(5, 4, 2, 64, "layer")
+
+
+def test_step_strides():
+    """A step's sequences may be further apart than a scan's tokens (a GPU test takes such a
+    step); here the limit behind that, and that nothing else gets past it."""
+    a = dict(x=1 << 16, a=1 << 16, b=1 << 16, A=1 << 16, t=1 << 16, st=1 << 16, N=3, D=64,
+             ldx=64, lda=64, ldb=64, dtype=1, flags=0, h=1 << 16, ldh=64)
+    for k in ("ldx", "lda", "ldb", "ldh"):
+        assert G.lib.gdn_linrec_step(*dict(a, **{k: 2 ** 32 + 1}).values(), None) == -2
+        assert G.lib.gdn_linrec_step(*dict(a, **{k: 2 ** 32, "N": -1}).values(), None) == -1
+    far = dict(a, ldx=2 ** 32, lda=2 ** 32, ldb=2 ** 32, N=0)
+    assert G.lib.gdn_linrec_step(*far.values(), None) == 0

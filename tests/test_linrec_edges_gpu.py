@@ -106,3 +106,21 @@ def test_every_argument_by_name_and_on_another_stream():
     P.check("h", h, *P.forward_bounds(*ins(s))["h"])
     P.check("dx", g["dx"], *P.backward_bounds(*ins(s, "dh", "dht"))["dx"])
     P.check("first", h1, *(v[:, 0] for v in P.forward_bounds(*ins(s))["h"]))
+
+
+def test_step_of_one_token_of_a_long_batch():
+    """Sequences further apart than a scan's tokens may be: a token of a [N, T, D] batch."""
+    N, T, D = 3, 1100, 2048  # 2.25M elements from sequence to sequence
+    s, d = make(N, 1, D, F32, seed=21)
+    want = P.forward_bounds(*ins(s))
+    far = {k: torch.zeros(N, T, D, device="cuda") for k in ("x", "a", "b")}
+    for k in far:
+        far[k][:, 700] = d[k][:, 0]
+    out = torch.zeros(N, T, D, device="cuda")
+    state = d["h0"].clone()
+    h = G.gdn_linrec_step(*(far[k][:, 700] for k in ("x", "a", "b")), d["A_log"], d["dt_bias"],
+                          state, h=out[:, 700])
+    P.check("h", h, want["h"][0][:, 0], want["h"][1][:, 0])
+    P.check("state", state, *want["ht"])
+    out[:, 700] = 0
+    assert not out.any()
