@@ -537,7 +537,8 @@ static int validate_linrec(const LinrecArgs& p, int more_flags, long long most_l
   const long long blocks = (p.D + 15) / 16;
   if (p.T > 1 << 30 || *chunks * blocks > 0x3fffffffLL || p.B * blocks > 0x3fffffffLL)
     return GDN_ERR_UNSUPPORTED;
-  if (p.ldx > most_ld || p.lda > most_ld || p.ldb > most_ld || p.D > 1 << 21)
+  if (p.ldx > most_ld || p.lda > most_ld || (p.b != nullptr && p.ldb > most_ld) ||
+      p.D > 1 << 21)
     return GDN_ERR_UNSUPPORTED;
   if (p.B == 0 || *chunks == 0) return GDN_OK;
   const size_t es = elem_size(p.dtype), ges = (p.flags & GDN_GATES_PRECOMPUTED) ? 4 : es;
@@ -625,7 +626,7 @@ int gdn_linrec_bwd(const void* x, const void* a, const void* b, const float* A_l
   if (!ok_elem(dh, ds) || lddh < D || !ok_elem(dx, ds) || lddx < D || !ok_elem(da, gs) ||
       ldda < D || (db != nullptr && (!ok_elem(db, gs) || lddb < D)))
     return GDN_ERR_INVALID_ARG;
-  if (lddh > kScanLd || lddx > kScanLd || ldda > kScanLd || lddb > kScanLd)
+  if (lddh > kScanLd || lddx > kScanLd || ldda > kScanLd || (db != nullptr && lddb > kScanLd))
     return GDN_ERR_UNSUPPORTED;
   if (!ok_workspace(workspace, ws_bytes,
                     linrec_bwd_workspace_bytes(cu_seqlens, B, T, D, states != nullptr, flags)))

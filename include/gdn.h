@@ -478,7 +478,8 @@ size_t gdn2_chunk_workspace_bytes(int B, int T, int H, int dk, int dv, int dtype
  * Gated DeltaNet" section 9), one per channel; the rule without keys is
  * S_t = alpha_t S_{t-1} + (input) of the pages' gated linear attention ("Qwen3.5",
  * GDN详解) with a vector in the place of the matrix.
- *   x, a, b    [B, T, D], or [T, D] packed with cu_seqlens: dtype, read; b NULL: beta = 1.
+ *   x, a, b    [B, T, D], or [T, D] packed with cu_seqlens: dtype, read; b NULL: beta = 1
+ *              (ldb unused).
  *              ldx, lda, ldb: elements from one token to the next (>= D; the rows of a
  *              batch follow one another, T * ld apart), so that slices of a fused
  *              projection are read where they are.

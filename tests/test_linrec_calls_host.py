@@ -67,3 +67,18 @@ def test_step_strides():
         assert G.lib.gdn_linrec_step(*dict(a, **{k: 2 ** 32, "N": -1}).values(), None) == -1
     far = dict(a, ldx=2 ** 32, lda=2 ** 32, ldb=2 ** 32, N=0)
     assert G.lib.gdn_linrec_step(*far.values(), None) == 0
+
+
+def test_the_distance_of_a_write_gate_that_is_not_there():
+    """ldb and lddb count with b and db alone (no token, so that nothing is launched; in the
+    backward the workspace's check, behind all others, ends the call)."""
+    p = 1 << 16
+    for b, st in ((None, 0), (p, -2)):
+        assert G.lib.gdn_linrec_fwd(p, p, b, p, p, None, None, 2, 0, 64, 64, 64, 2 ** 30, 1, 0, p,
+                                    64, None, None, None, 0, None) == st
+        assert G.lib.gdn_linrec_step(p, p, b, p, p, p, 0, 64, 64, 64, 2 ** 33, 1, 0, p, 64,
+                                     None) == st
+    for db, st in ((None, -5), (p, -2)):
+        assert G.lib.gdn_linrec_bwd(p, p, db, p, p, None, None, 2, 100, 64, 64, 64, 64, p, 64, None,
+                                    p, 1, 0, p, 64, p, 64, db, 2 ** 30, p, p, None, None, 0,
+                                    None) == st
