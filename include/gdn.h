@@ -505,8 +505,9 @@ size_t gdn2_chunk_workspace_bytes(int B, int T, int H, int dk, int dv, int dtype
  *   aligned come by TMA).  At most 2^30 tokens, D and every ld at most 2^21, and fewer
  *   than 2^30 pairs of a chunk and 16 channels: else GDN_ERR_UNSUPPORTED.  States and
  *   sums are float32, outputs rounded once; the result does not depend on how the work
- *   was split.  T = 0 and empty sequences copy h0 to ht
- *   (or zeros).  Long sequences of few channels are taken by clusters of thread blocks
+ *   was split.  NaN goes through as in the formulas; an infinite state has no finite
+ *   value behind it, but may become NaN there (products of decays that underflow are 0).
+ *   T = 0 and empty sequences copy h0 to ht (or zeros).  Long sequences of few channels are taken by clusters of thread blocks
  *   that wait for one another, with a limit: an expired wait is reported by
  *   gdn_check_status.
  */

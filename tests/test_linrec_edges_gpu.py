@@ -124,3 +124,47 @@ def test_step_of_one_token_of_a_long_batch():
     P.check("state", state, *want["ht"])
     out[:, 700] = 0
     assert not out.any()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("scale", ["none", "unit"])
+def test_infinities(dtype, scale):
+    """An infinite input or state leaves its channel without a finite value from there on (NaN
+    where products of decays have underflowed, as 0 x inf) and reaches nothing else; so does an
+    infinite gradient, the other way."""
+    s, d = make(2, 260, 70, dtype, seed=19)
+    d["A_log"][33:36] = 2.7  # fast channels: 8 tokens' product of decays is 0
+    for c in (33, 34):
+        d["a"][:, :, c] = 5.0
+    kw = dict(input_scale=scale)
+    h, ht = G.gdn_linrec_fwd(*ins(d), **kw)
+    g = G.gdn_linrec_bwd(*ins(d), d["dh"], d["dht"], **kw)
+    e = dict(d, x=d["x"].clone(), h0=d["h0"].clone())
+    e["x"][1, 100, 33] = float("inf")
+    e["x"][0, 70, 35] = float("-inf")
+    e["h0"][0, 34] = float("inf")
+    h2, ht2 = G.gdn_linrec_fwd(*ins(e), **kw)
+    bad = torch.zeros_like(h, dtype=torch.bool)
+    bad[1, 100:, 33] = bad[0, 70:, 35] = bad[0, :, 34] = True
+    assert torch.equal(~torch.isfinite(h2), bad)
+    assert torch.equal(h2[~bad], h[~bad])
+    assert torch.equal(~torch.isfinite(ht2), bad[:, -1]) and torch.equal(ht2[~bad[:, -1]],
+                                                                         ht[~bad[:, -1]])
+    g2 = G.gdn_linrec_bwd(*ins(e), d["dh"], d["dht"], **kw)
+    assert torch.equal(g2["dx"], g["dx"]) and torch.equal(g2["dh0"], g["dh0"])
+    assert torch.equal(g2["da"][~bad], g["da"][~bad])
+    one = torch.zeros_like(bad)
+    one[1, 100, 33] = one[0, 70, 35] = True
+    assert torch.equal(g2["db"][~one], g["db"][~one])
+    e = dict(d, dh=d["dh"].clone(), dht=d["dht"].clone())
+    e["dh"][1, 100, 33] = float("inf")
+    e["dht"][0, 34] = float("-inf")
+    g2 = G.gdn_linrec_bwd(*ins(e), e["dh"], e["dht"], **kw)
+    bad = torch.zeros_like(bad)
+    bad[1, :101, 33] = bad[0, :, 34] = True
+    for k in ("dx", "da", "db"):
+        assert torch.equal(g2[k][~bad], g[k][~bad]), k
+        assert not torch.isfinite(g2[k][bad]).any(), k
+    rest = ~bad[:, 0]
+    assert not torch.isfinite(g2["dh0"][~rest]).any() and torch.equal(g2["dh0"][rest],
+                                                                      g["dh0"][rest])
