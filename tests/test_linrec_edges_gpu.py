@@ -168,3 +168,26 @@ def test_infinities(dtype, scale):
     rest = ~bad[:, 0]
     assert not torch.isfinite(g2["dh0"][~rest]).any() and torch.equal(g2["dh0"][rest],
                                                                       g["dh0"][rest])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_what_a_workspace_holds_before_the_call_does_not_matter(dtype):
+    """A packed batch's table, the states and the blocks' sums, over memory of any content."""
+    cu = [0, 130, 130, 131, 700, 1500]
+    _, d = make(len(cu) - 1, cu[-1], 88, dtype, cu=cu, seed=20)
+    size = (len(cu) - 1, cu[-1], 88, cu)
+    need, more = G.gdn_linrec_workspace_bytes(*size), G.gdn_linrec_bwd_workspace_bytes(*size)
+    assert more > need > 0
+    h, ht = G.gdn_linrec_fwd(*ins(d), cu_seqlens=cu)
+    g = G.gdn_linrec_bwd(*ins(d), d["dh"], d["dht"], cu_seqlens=cu)
+    for fill in (0, 1, 127, 255):
+        ws = torch.full((need,), fill, dtype=torch.uint8, device="cuda")
+        h2, ht2 = G.gdn_linrec_fwd(*ins(d), cu_seqlens=cu, workspace=ws)
+        assert torch.equal(h, h2) and torch.equal(ht, ht2)
+        ws = torch.full((more,), fill, dtype=torch.uint8, device="cuda")
+        g2 = G.gdn_linrec_bwd(*ins(d), d["dh"], d["dht"], cu_seqlens=cu, workspace=ws)
+        assert all(torch.equal(g[k], g2[k]) for k in g)
+    with pytest.raises(G.GDNError):
+        G.gdn_linrec_fwd(*ins(d), cu_seqlens=cu, workspace=ws[:need - 1])
+    with pytest.raises(G.GDNError):
+        G.gdn_linrec_bwd(*ins(d), d["dh"], cu_seqlens=cu, workspace=ws[:more - 1])
