@@ -40,7 +40,6 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
 __device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
-__device__ __forceinline__ float2 held(float v) { return make_float2(v, v); }
 __device__ __forceinline__ float2 ex2_2(float2 x) { return make_float2(ex2_f(x.x), ex2_f(x.y)); }
 __device__ __forceinline__ float2 rcp_2(float2 x) { return make_float2(rcp_f(x.x), rcp_f(x.y)); }
 
@@ -52,12 +51,12 @@ __device__ __forceinline__ void log1p_over(const float2* y, float2* p) {
   const float k[9] = {5.232694263e-03f, -2.950523877e-02f, 7.822595187e-02f,
                       -1.366324579e-01f, 1.910600676e-01f, -2.484298221e-01f,
                       3.331909681e-01f, -4.999949314e-01f, 9.999999699e-01f};
-  const float2 k0 = held(k[0]), k1 = held(k[1]);
+  const float2 k0 = both(k[0]), k1 = both(k[1]);
 #pragma unroll
   for (int i = 0; i < N; ++i) p[i] = fma2(y[i], k0, k1);
 #pragma unroll
   for (int j = 2; j < 9; ++j) {
-    const float2 kj = held(k[j]);
+    const float2 kj = both(k[j]);
 #pragma unroll
     for (int i = 0; i < N; ++i) p[i] = fma2(p[i], y[i], kj);
   }
@@ -70,12 +69,12 @@ template <int N>
 __device__ __forceinline__ void one_minus_ex2(const float2* e, const float2* pow, float2* f) {
   const float k[5] = {-1.15445233e-03f, -9.54128150e-03f, -5.54904081e-02f, -2.40225643e-01f,
                       -6.93147182e-01f};
-  const float2 k0 = held(k[0]), k1 = held(k[1]);
+  const float2 k0 = both(k[0]), k1 = both(k[1]);
 #pragma unroll
   for (int i = 0; i < N; ++i) f[i] = fma2(e[i], k0, k1);
 #pragma unroll
   for (int j = 2; j < 5; ++j) {
-    const float2 kj = held(k[j]);
+    const float2 kj = both(k[j]);
 #pragma unroll
     for (int i = 0; i < N; ++i) f[i] = fma2(e[i], f[i], kj);
   }
@@ -133,7 +132,7 @@ template <int N>
 __device__ __forceinline__ void decay_exponents_slope(float2* a, const GateConst& k,
                                                       float2* slope) {
   float2 y[N], q[N];
-  const float2 rate = mul2(k.rate, both(kLn2)), one = held(1.f);
+  const float2 rate = mul2(k.rate, both(kLn2)), one = both(1.f);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     a[i] = add2(a[i], k.bias);
@@ -150,12 +149,12 @@ __device__ __forceinline__ void decay_exponents_slope(float2* a, const GateConst
   }
 }
 
-// The input scales f of N tokens from alpha = 2^e.
+// The input scales f of N tokens from alpha = 2^e (not called for kScaleNone).
 template <int SCALE, int N>
 __device__ __forceinline__ void input_scales(const float2* e, const float2* alpha, float2* f) {
   if (SCALE == kScaleTied) {
     one_minus_ex2<N>(e, alpha, f);
-  } else if (SCALE == kScaleUnit) {
+  } else {
     float2 e2[N], a2[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -165,9 +164,6 @@ __device__ __forceinline__ void input_scales(const float2* e, const float2* alph
     one_minus_ex2<N>(e2, a2, f);
 #pragma unroll
     for (int i = 0; i < N; ++i) f[i] = make_float2(sqrt_f(f[i].x), sqrt_f(f[i].y));
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = both(1.f);
   }
 }
 // df/dg.  sqrt(1 - alpha^2) has an infinite slope at g = 0; what reaches a is f' dg/da, which
@@ -175,15 +171,14 @@ __device__ __forceinline__ void input_scales(const float2* e, const float2* alph
 template <int SCALE>
 __device__ __forceinline__ float input_scale_slope(float alpha, float f) {
   if (SCALE == kScaleTied) return -alpha;
-  if (SCALE == kScaleUnit) return f > 0.f ? -alpha * alpha * rcp_f(f) : 0.f;
-  return 0.f;
+  return f > 0.f ? -alpha * alpha * rcp_f(f) : 0.f;
 }
 
 // beta[i] in place of b[i]; GIVEN: b is beta itself.
 template <bool GIVEN, int N>
 __device__ __forceinline__ void write_gates(float2* b) {
   if (GIVEN) return;
-  const float2 one = held(1.f);
+  const float2 one = both(1.f);
 #pragma unroll
   for (int i = 0; i < N; ++i)
     b[i] = rcp_2(add2(make_float2(ex2_f(b[i].x * -kLog2e), ex2_f(b[i].y * -kLog2e)), one));
