@@ -90,3 +90,22 @@ def test_positions_of_many_bits(bits, theta, interleaved):
         rad = 6.2831853072 * far * 2.0 ** -65
         P.check(f"{name} at 2^{bits}", got, y,
                 (8 * P.U + rad) * P.rope_pair_size(x, d, interleaved))
+
+
+def test_frequencies_of_any_size_and_sign():
+    """Whole turns a token, none at all, the other way round: the bound of above."""
+    s, dev = R.make(40, 2, 1, 16, 16, F32, seed=1, far=1 << 24, weights=False)
+    freq = torch.tensor([0.0, 1e-30, -1e-30, 1e-9, -0.37, 6.2831855, 12345.678, -7e6])
+    s["inv_freq"] = freq
+    unit = Fraction(two_pi(256), 1 << 256)
+    ang = torch.tensor([[float((t - round(t)) * unit) for t in (p * Fraction(f) / unit
+                                                                for f in freq.tolist())]
+                        for p in s["pos"].tolist()], dtype=F64)
+    c, sn = ang.cos()[:, None], ang.sin()[:, None]
+    outs = G.gdn_qk_norm_rope(dev["q"], dev["k"], dev["pos"], freq.cuda(), norm=None)
+    for name, got in zip("qk", outs):
+        x = s[name].to(F64)
+        p, q = x[..., :8], x[..., 8:]
+        y = torch.cat([p * c - q * sn, q * c + p * sn], -1)
+        rad = 6.2831853072 * s["pos"].to(F64)[:, None, None] * 2.0 ** -65
+        P.check(name, got, y, (8 * P.U + rad) * P.rope_pair_size(x, 16, False))
