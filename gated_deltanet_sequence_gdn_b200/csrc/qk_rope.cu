@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(kThreads, 3) qk_rope_kernel(const __grid_const
   int hb = a.part * NH * U;
   Raw<T> raw[U];
   load(hb, raw);  // on the way while the angles are evaluated
-  block_angles(p, toks, t0, sm);
+  block_angles(p, toks, t0, sm, [&](int i) { return turn_fraction(p.inv_freq[i]); });
   load_weights(p, true, sm);
   __syncthreads();
   if (t >= p.tokens) return;

@@ -154,14 +154,16 @@ __device__ __forceinline__ void lane_begin(const Sides& p, Lane& L) {
   L.src = L.e0 < half ? lane + half / 8 : L.e0 < p.rot ? lane - half / 8 : lane;
 }
 
-// Evaluates the angles of `toks` tokens from t0 on (every thread calls it).
-__device__ __forceinline__ void block_angles(const Sides& p, int toks, long long t0, Smem& sm) {
+// Evaluates the angles of `toks` tokens from t0 on (every thread calls it); turn(i): pair i's
+// turn_fraction.
+template <typename Turn>
+__device__ __forceinline__ void block_angles(const Sides& p, int toks, long long t0, Smem& sm,
+                                             const Turn& turn) {
   const int half = p.rot / 2;
   for (int j = threadIdx.x; j < half * toks; j += kThreads) {
     const int tk = j / half, i = j - tk * half;
     if (t0 + tk >= p.tokens) break;
-    const unsigned long long ph =
-        (unsigned long long)p.positions[t0 + tk] * turn_fraction(p.inv_freq[i]);
+    const unsigned long long ph = (unsigned long long)p.positions[t0 + tk] * turn(i);
     float sn, cn;
     sincospif((float)(int)(ph >> 32) * 4.656612873077393e-10f, &sn, &cn);  // 2^-31 half turns
     sm.cs[tk][i] = cn;
@@ -248,8 +250,8 @@ __device__ __forceinline__ void rotate(const Sides& p, const Lane& L, float* swa
   // A whole head's turn needs no look at the lane, where the head fills its lanes' channels: in a
   // lane that it ends in, the angles behind the last pair are not there, and 0 (the channels
   // behind the head) times what the shared memory holds may be NaN, which the backward's sums
-  // would take to the rest of the head.
-  if (L.turned == 8 || (p.rot == p.d && p.d % 8 == 0)) {
+  // would take to the rest of the head.  kPairShuffle takes whole lanes only.
+  if ((p.rot == p.d && (PAIRS == kPairShuffle || p.d % 8 == 0)) || L.turned == 8) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) y[i] = fma2(o[i], L.s[i], mul2(y[i], L.c[i]));
   } else if (PAIRS != kPairShuffle && L.turned > 0) {

@@ -19,6 +19,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 qk_rope_bwd_kernel(const __grid_constant__ Sides p, float* partial) {
   __shared__ __align__(16) Smem sm;
   __shared__ float wsum[kWarps][256];
+  __shared__ unsigned long long turns[kMaxHalf];  // formed once: the block takes many tokens
   constexpr int NH = 32 / GROUP;
   constexpr int U = 2;
   const Place a = place_of(p);
@@ -28,6 +29,7 @@ qk_rope_bwd_kernel(const __grid_constant__ Sides p, float* partial) {
   Lane L;
   lane_begin<GROUP>(p, L);
   load_weights(p, false, sm);
+  for (int i = threadIdx.x; i < p.rot / 2; i += kThreads) turns[i] = turn_fraction(p.inv_freq[i]);
   const int off = grp * p.d + L.e0;
   float2 dw[4];
 #pragma unroll
@@ -50,8 +52,8 @@ qk_rope_bwd_kernel(const __grid_constant__ Sides p, float* partial) {
     Raw<T> rx[U];
     Raw<TG> rg[U];
     load(hb, rx, rg);  // on the way while the angles are evaluated
-    __syncthreads();   // the last tokens' angles are read
-    block_angles(p, toks, t0, sm);
+    __syncthreads();   // the turns are there, the last tokens' angles read
+    block_angles(p, toks, t0, sm, [&](int i) { return turns[i]; });
     __syncthreads();
     if (t >= p.tokens) continue;
     lane_angles<PAIRS>(p, sm.cs[a.token], sm.sn[a.token], true, L);
