@@ -179,17 +179,22 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
           Hm = H;
         }
       }
+      // lambda from token to token, R = alpha lambda of the first.  dh + alpha lambda is written as
+      // the fma that the compiler makes of it in some of these loops and not in others: the
+      // gradients' last bits would go by the loop, that is by the tile's shape.
       if (n == kTileT) {
+        R = get2(st.dh + mine + (kPer - 1) * kC);
 #pragma unroll
-        for (int i = kPer - 1; i >= 0; --i)
-          R = mul2(al[i], add2(get2(st.dh + mine + i * kC), R));
+        for (int i = kPer - 2; i >= 0; --i)
+          R = fma2(al[i + 1], R, get2(st.dh + mine + i * kC));
       } else {
 #pragma unroll
         for (int i = kPer - 1; i >= 0; --i) {
-          if (first + i < n) R = add2(get2(st.dh + mine + i * kC), R);
-          R = mul2(al[i], R);
+          const float2 dh = first + i < n ? get2(st.dh + mine + i * kC) : both(0.f);
+          R = i == kPer - 1 ? dh : fma2(al[i + 1], R, dh);
         }
       }
+      R = mul2(al[0], R);
       sm.carry.fold[threadIdx.x] = join4(A, H);
       sm.back[threadIdx.x] = R;
     }
@@ -221,7 +226,8 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
     }
     __syncthreads();
     hs = sm.start[threadIdx.x];
-    float2 cc = sm.back[threadIdx.x];
+    // lambda, and alpha, of the token behind (of none: what arrives from there)
+    float2 lam = sm.back[threadIdx.x], behind = both(1.f);
     float2 tA = both(0.f), tb = both(0.f);
     // The later group of tokens first; its states from the one in front of it.
 #pragma unroll
@@ -239,8 +245,9 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
       }
       auto token = [&](int j, float2* dx, float2* da, float2* db) {
         const int i = i0 + j, el = mine + i * kC;
-        const float2 lam = add2(get2(st.dh + el), cc);
-        cc = mul2(al[j], lam);
+        lam = fma2(behind, lam, get2(st.dh + el));
+        behind = al[j];
+        const float2 cc = mul2(al[j], lam);
         const float2 lx = mul2(lam, get2(st.x + el));
         float2 dg = mul2(cc, hp[j]);
         *dx = mul2(lam, be[i]);
@@ -256,7 +263,7 @@ linrec_bwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
         if (!GIVEN) {
           if (p.b) *db = mul2(mul2(*db, be[i]), write_gate_rest(get2(st.b + el), be[i]));
           *da = mul2(dg, slope[i]);
-          tb = add2(tb, *da);
+          tb = fma2(dg, slope[i], tb);
           // dg log2(e) times e, which is -inf where alpha = 0
           tA = fma2(dg, make_float2(fmaxf(e[i].x, -3e38f), fmaxf(e[i].y, -3e38f)), tA);
         }

@@ -536,12 +536,13 @@ size_t gdn_linrec_workspace_bytes(const long long* cu_seqlens, int B, int T, int
  *   dx, da, db [B, T, D] or [T, D] dtype (float32 with GDN_GRAD_F32; da and db always
  *     float32 with GDN_GATES_PRECOMPUTED, where they are the gradients at g and beta),
  *     written; db NULL exactly when b is; they must not overlap the inputs or each other
- *   dA_log, ddt_bias [D] float32, written (sums over all tokens, in a fixed order);
- *     unused with GDN_GATES_PRECOMPUTED
+ *   dA_log, ddt_bias [D] float32, written (sums over all tokens, in an order that is fixed
+ *     for the call's sizes); unused with GDN_GATES_PRECOMPUTED
  *   dh0    [B, D] float32, written; NULL = not stored; may be dht
  *   flags      GDN_GATES_PRECOMPUTED, GDN_GRAD_F32, GDN_LINREC_TIED or GDN_LINREC_UNIT
  *   workspace / ws_bytes: as above, sized by gdn_linrec_bwd_workspace_bytes.
- * Tokens behind the last packed sequence are left as they were.
+ * Tokens behind the last packed sequence are left as they were.  dx, da, db and dh0 do not
+ * depend on how the work was split.
  */
 int gdn_linrec_bwd(const void* x, const void* a, const void* b, const float* A_log,
                    const float* dt_bias, const float* h0, const long long* cu_seqlens, int B,

@@ -191,3 +191,30 @@ def test_what_a_workspace_holds_before_the_call_does_not_matter(dtype):
         G.gdn_linrec_fwd(*ins(d), cu_seqlens=cu, workspace=ws[:need - 1])
     with pytest.raises(G.GDNError):
         G.gdn_linrec_bwd(*ins(d), d["dh"], cu_seqlens=cu, workspace=ws[:more - 1])
+
+
+@pytest.mark.parametrize("T", [1, 65, 100, 192, 250, 300])
+@pytest.mark.parametrize("scale,gate,given", [("none", True, False), ("tied", False, False),
+                                              ("unit", True, True)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_gradients_do_not_depend_on_the_split(dtype, scale, gate, given, T):
+    """A sequence in a batch that fills the machine (tiles of one chunk, lone blocks), by itself
+    (tiles of several chunks, ends inside them, clusters), and with a channel more (rows whose
+    pairs are not aligned and that no TMA takes): bit for bit the same."""
+    B, D = 700, 64
+    _, d = make(B, T, D, dtype, gate=gate, given=given, seed=T)
+    kw = dict(input_scale=scale, gates_precomputed=given, grad_f32=True)
+
+    def grads(s):
+        g = G.gdn_linrec_bwd(*ins(s), s["dh"].float(), s["dht"], **kw)
+        return {k: g[k] for k in ("dx", "da", "db", "dh0") if g[k] is not None}
+
+    want = grads(d)
+    seq = ("x", "a", "b", "dh", "h0", "dht")
+    for r in (0, B - 1):
+        one = {k: v[r:r + 1] if k in seq and v is not None else v for k, v in d.items()}
+        for k, v in grads(one).items():
+            assert torch.equal(v, want[k][r:r + 1]), k
+    wide = {k: None if v is None else torch.cat([v, v[..., :1]], -1) for k, v in d.items()}
+    for k, v in grads(wide).items():
+        assert torch.equal(v[..., :D], want[k]), k
