@@ -7,11 +7,11 @@
 // instructions, most of them softplus, two exponentials and a sigmoid, against the 44 that an
 // SM issues while 8 bytes cross its share of the HBM at the measured copy rate; 60% of the
 // issue slots and of the XU pipe are in use at 27 warps an SM.  float32 (16 bytes) is bound by
-// the HBM alone.  Measured: 64 sequences of 512 x 4096 bf16 179 us, 6.0 TB/s (copy: 6.6);
+// the HBM alone.  Measured: 64 sequences of 512 x 4096 bf16 181 us, 5.9 TB/s (copy: 6.6);
 // float32 of 512 x 2048 160 us, 6.7 TB/s.  Where there are few chains, their blocks do not
 // share evenly among the SMs and wait more for their own carry: one sequence of 8192 x 12288
-// 182 us, 4.4 TB/s; 131072 x 1024, tied, without a write gate (6 bytes), in clusters 285 us,
-// 2.8 TB/s.
+// 184 us on the same inputs again and 197 on others each time (4.4 and 4.1 TB/s); 131072 x
+// 1024, tied, without a write gate (6 bytes), in clusters 280 us, 2.9 TB/s.
 //
 // Three barriers a tile: the stage is there; the folds are; the start states are.  One warp
 // joins the folds while the others wait.  Every warp finding its own start state takes one
@@ -215,7 +215,8 @@ linrec_fwd_kernel(LinrecArgs p, Chains ch, int vec, const __grid_constant__ Linr
 // The step: HBM-bound on the float32 state, read and written once.  A thread takes 4 channels
 // of one sequence, in pieces of 4 elements (VEC: the rows are aligned to them) or one by one.
 // 16 bytes a bf16 channel with a write gate: 4096 x 4096 44 us, 6.1 TB/s; 256 x 12288 10.4 us
-// in a graph, 4.8 TB/s, where one wave's latency counts; two channels a thread took 2.6 us more.
+// in a graph, 4.8 TB/s (6144 blocks, 2.6 times what runs at once: the launch, the first loads'
+// latency and the unfilled last wave count); two channels a thread took 2.6 us more.
 template <bool VEC, typename T>
 __device__ __forceinline__ void take4(const void* base, long long at, int cols, float2* f) {
   const T* p = static_cast<const T*>(base) + at;

@@ -122,13 +122,16 @@ inline long long chains_of(const LinrecArgs& p, int split) {
 // the share of a tile's channels that exist.  Chains that fill the machine run without
 // clusters (608 to 704 chains of 4096 tokens take the same 286 us; in clusters, which end in a
 // smaller last wave, 286 to 341); fewer run in the largest cluster whose launch still runs at
-// once, and the smaller cluster (fewer exchanges) is taken where shapes are equal.  Forward, us
-// by shape (chunks of a tile x blocks of a cluster):
+// once, and the smaller cluster (fewer exchanges) is taken where shapes are equal.  That is
+// not always the faster of the equal ones: 32768 x 2048 would gain 8% from 2x6, where 8192 x
+// 4096 and 8192 x 12288 lose or gain nothing by the larger cluster; what an exchange costs is
+// not weighed against the longer rows of a wider tile.  Forward, us by shape (chunks of a tile
+// x blocks of a cluster):
 //   8192 tokens x 12288 channels  1x2 200, 1x3 224, 2x1 185, 2x2 192, 4x1 183 (taken, 768 blocks)
 //   8192 x 8192                   1x3 143, 2x2 129, 4x1 123 (taken)
 //   8192 x 4096                   1x6 80, 2x3 80, 4x1 80, 4x2 78 (taken)
 //   32768 x 2048                  1x8 174, 2x6 153, 4x3 166 (taken), 4x6 178
-//   131072 x 1024, tied           1x16 440, 2x8 363, 4x6 319, 4x8 297 (taken, 284 by now)
+//   131072 x 1024, tied           1x16 440, 2x8 363, 4x6 319, 4x8 297 (taken, 280 by now)
 //   43 x 3699 x 14                53 in tiles of 64 channels, 22 of 16 (taken)
 template <typename K>
 cudaError_t choose_split(const LinrecArgs& p, const ChainKernel<K> (&ks)[3], size_t smem,

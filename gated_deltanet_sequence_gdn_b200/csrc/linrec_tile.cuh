@@ -2,7 +2,7 @@
 // its backward share: tiles of tokens x channels, their rows copied to shared memory ahead of
 // use, and the carry from tile to tile.
 //
-// A chain is one sequence's 64 channels (or 32: Shape); its tiles are taken in turn by the
+// A chain is one sequence's 64 channels (or 32, or 16: Shape); its tiles are taken in turn by the
 // blocks of one thread-block cluster (1 to 16 blocks: as many as it takes to fill the
 // machine).  A lane holds 2 adjacent channels of 8 tokens.  Each thread folds its 8 tokens
 // into (A, H): carry_out = A carry_in + H; the folds of a chunk's 8 groups of tokens meet in

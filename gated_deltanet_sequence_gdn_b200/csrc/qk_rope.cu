@@ -2,7 +2,7 @@
 //
 // What bounds it: 15.5 instructions an element against 4 bytes of bf16 (the time of 22), at 57%
 // of the issue slots with 21 warps an SM, which wait for their loads between rounds of heads.
-// Measured, 16 + 16 heads of 128, bf16: 8192 tokens 31 us, 4.3 TB/s; 65536 tokens 205 us, 5.2
+// Measured, 16 + 16 heads of 128, bf16: 8192 tokens 31 us, 4.3 TB/s; 65536 tokens 206 us, 5.2
 // TB/s.  A head at a time took 77 us at 8192 tokens; four on the way 49; q and k by warps of
 // the same block, the kind of pairs at compile time and the loads ahead of the angles 31.
 // Eight on the way with two blocks an SM take 35, two with four blocks 36.

@@ -5,7 +5,7 @@
 //
 // What bounds it: 25 instructions an element against 6 bytes of bf16 (the time of 33), at 55% of
 // the issue slots with the 15 warps an SM that 123 registers leave.  Measured, 16 + 16 heads of
-// 128, bf16, with the launch that joins the weights' gradients: 8192 tokens 53 us, 3.8 TB/s;
+// 128, bf16, with the launch that joins the weights' gradients: 8192 tokens 51 us, 3.9 TB/s;
 // 65536 tokens 328 us, 4.9 TB/s.  Three blocks an SM spill (69 against 61 us at the time).
 #include "qk_rope.cuh"
 
@@ -148,7 +148,8 @@ qk_rope_sums_kernel(const float* partial, int blocks, int d, float* dqw, float* 
 }
 
 // The backward's blocks loop over the tokens (they keep their share of the weights'
-// gradients): two a multiprocessor.
+// gradients): two on each of the 148 multiprocessors of the chip that this is built for.  The
+// workspace's size goes by them, and is asked for without a device.
 constexpr int kBwdBlocks = 148 * 2;
 void plan_bwd(Sides* p) {
   plan_warps(p, 2, 4);
