@@ -14,7 +14,7 @@
 // us).  dA_log and ddt_bias are summed by the lanes that hold their channels, rounding errors
 // kept, and joined over the blocks in a fixed order.
 //
-// What bounds it: 65 instructions an element against 14 bytes of bf16, at 55% of the issue
+// What bounds it: 66 instructions an element against 14 bytes of bf16, at 56% of the issue
 // slots with 15 warps an SM.  Measured: 64 sequences of 512 x 4096 bf16 421 us, 4.5 TB/s;
 // float32 of 512 x 2048 360 us, 5.2 TB/s; 131072 x 1024 without a write gate 461 us, 2.9 TB/s.
 #include "linrec_launch.cuh"

@@ -1,6 +1,6 @@
 // qk_rope.cu -- norm and rotation of q and k (qk_rope.cuh), forward.
 //
-// What bounds it: 15.5 instructions an element against 4 bytes of bf16 (the time of 22), at 57%
+// What bounds it: 15.7 instructions an element against 4 bytes of bf16 (the time of 22), at 57%
 // of the issue slots with 21 warps an SM, which wait for their loads between rounds of heads.
 // Measured, 16 + 16 heads of 128, bf16: 8192 tokens 31 us, 4.3 TB/s; 65536 tokens 206 us, 5.2
 // TB/s.  A head at a time took 77 us at 8192 tokens; four on the way 49; q and k by warps of
