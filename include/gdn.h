@@ -507,9 +507,9 @@ size_t gdn2_chunk_workspace_bytes(int B, int T, int H, int dk, int dv, int dtype
  *   sums are float32, outputs rounded once; the result does not depend on how the work
  *   was split.  NaN goes through as in the formulas; an infinite state has no finite
  *   value behind it, but may become NaN there (products of decays that underflow are 0).
- *   T = 0 and empty sequences copy h0 to ht (or zeros).  Long sequences of few channels are taken by clusters of thread blocks
- *   that wait for one another, with a limit: an expired wait is reported by
- *   gdn_check_status.
+ *   T = 0 and empty sequences copy h0 to ht (or zeros).  Long sequences of few channels
+ *   are taken by clusters of thread blocks that wait for one another, with a limit: an
+ *   expired wait is reported by gdn_check_status.
  */
 int gdn_linrec_fwd(const void* x, const void* a, const void* b, const float* A_log,
                    const float* dt_bias, const float* h0, const long long* cu_seqlens, int B,
